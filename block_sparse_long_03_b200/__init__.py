@@ -27,7 +27,8 @@ __all__ = [
     "msa_selftest_wait_timeout", "msa_sparse_attn_fwd", "msa_profile_begin", "msa_profile_end",
     "msa_bounds_failures",
     "msa_topk_blocks", "msa_workspace_size", "params_from", "sparse_attn_fwd", "status_string",
-    "topk_blocks",
+    "topk_blocks", "rope", "rope_frequencies", "rope_append_paged", "attn_packed", "attn_paged",
+    "RopeParams", "AttnParams",
 ]
 
 

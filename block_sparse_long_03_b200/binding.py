@@ -24,7 +24,9 @@ MSA_WS_SPARSE_ATTN, MSA_WS_FORWARD, MSA_WS_FORWARD_HOST, MSA_WS_DECODE_PAGED = 0
 MSA_WS_INDEX_HIER = 4
 STATUS_NAMES = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_CUDA",
                 4: "MSA_ERR_DEVICE_TIMEOUT", 5: "MSA_ERR_WORKSPACE", 6: "MSA_ERR_BAD_BLOCK_IDS",
-                7: "MSA_ERR_BAD_PAGE_TABLE"}
+                7: "MSA_ERR_BAD_PAGE_TABLE", 8: "MSA_ERR_BAD_OFFSETS"}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 # Every symbol the header declares (checked by the CPU test suite).
 EXPORTS = ("msa_status_string", "msa_index_block_scores", "msa_topk_blocks",
@@ -32,7 +34,9 @@ EXPORTS = ("msa_status_string", "msa_index_block_scores", "msa_topk_blocks",
            "msa_kernel_launches", "msa_forward_noalloc", "msa_forward_host",
            "msa_selftest_wait_timeout", "msa_sparse_attn_fwd_mass", "msa_forward_mass",
            "msa_query_pieces", "msa_decode_paged", "msa_index_hierarchical",
-           "msa_bounds_failures", "msa_profile_begin", "msa_profile_end")
+           "msa_bounds_failures", "msa_profile_begin", "msa_profile_end",
+           "msa_rope_frequencies", "msa_rope", "msa_rope_append_paged",
+           "msa_attn_workspace_size", "msa_attn_packed", "msa_attn_paged")
 
 
 class MsaError(RuntimeError):
@@ -46,6 +50,24 @@ class Params(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("B", "T", "S", "Hq", "Hkv", "d", "d_idx", "block", "topk", "dtype")] + \
                [("scale", ctypes.c_float)]
+
+
+class RopeParams(ctypes.Structure):
+    """msa_rope_params_t."""
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("tokens", "q_stride", "k_stride", "q_out_stride", "k_out_stride")] + \
+               [(n, ctypes.c_int32) for n in
+                ("Hq", "Hkv", "d", "rot_dim", "layout", "inverse", "dtype")] + \
+               [("mscale", ctypes.c_float)]
+
+
+class AttnParams(ctypes.Structure):
+    """msa_attn_params_t."""
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("tokens", "key_tokens", "q_stride", "k_stride", "v_stride")] + \
+               [(n, ctypes.c_int32) for n in ("B", "Hq", "Hkv", "d", "dtype")] + \
+               [("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("page_size", "max_pages", "num_pages")]
 
 
 def _load():
@@ -85,6 +107,19 @@ def _load():
     lib.msa_kernel_launches.restype = ctypes.c_uint64
     lib.msa_bounds_failures.argtypes = []
     lib.msa_bounds_failures.restype = ctypes.c_uint32
+    dbl, i64, RP, AP = ctypes.c_double, ctypes.c_int64, ctypes.POINTER(RopeParams), \
+        ctypes.POINTER(AttnParams)
+    lib.msa_rope_frequencies.argtypes = [i32, dbl, i32, dbl, dbl, dbl, dbl, vp]
+    lib.msa_rope.argtypes = [RP] + [vp] * 7
+    lib.msa_rope_append_paged.argtypes = [RP, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp, i64, vp,
+                                          i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.msa_attn_workspace_size.argtypes = [AP, ctypes.c_int]
+    lib.msa_attn_workspace_size.restype = sz
+    lib.msa_attn_packed.argtypes = [AP] + [vp] * 8 + [sz, vp]
+    lib.msa_attn_paged.argtypes = [AP] + [vp] * 9 + [sz, vp]
+    for name in ("msa_rope_frequencies", "msa_rope", "msa_rope_append_paged", "msa_attn_packed",
+                 "msa_attn_paged"):
+        getattr(lib, name).restype = st
     lib.msa_profile_begin.argtypes = []
     lib.msa_profile_begin.restype = st
     lib.msa_profile_end.argtypes = [vp, vp, vp, vp]
@@ -352,3 +387,218 @@ def index_hierarchical(q_idx, k_idx, *, block: int, topk: int, kc: int):
     ws = alloc_workspace(p, MSA_WS_INDEX_HIER, q_idx.device)
     msa_index_hierarchical(p, kc, q_idx, k_idx, ids, ws)
     return ids, ws
+
+
+# ---- serving operators: rotary positions, the paged cache write, full attention ----
+
+_DTYPE_CODES = {torch.float32: MSA_F32, torch.bfloat16: MSA_BF16}
+
+
+def _refuse(where: str, why: str):
+    raise MsaError(1, f"{where} ({why})")
+
+
+def _tokens(where, name, t, like=None):
+    """The token stride of t [tokens, heads, d], whose heads are dense."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        _refuse(where, f"{name} must be [tokens, heads, d] with dense heads")
+    if t.dtype not in _DTYPE_CODES or (like is not None and (t.dtype != like.dtype or
+                                                             t.device != like.device)):
+        _refuse(where, f"{name}: dtype or device")
+    if t.shape[0] <= 1:
+        return 0
+    if t.stride(0) == 0:
+        _refuse(where, f"{name}: expanded over tokens")
+    return t.stride(0)
+
+
+def _dense(where, name, t, dtype, device, shape):
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        _refuse(where, f"{name} must be dense {dtype} {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _on_device(where, device, call, *args):
+    """call(*args, stream) on the current stream of `device`."""
+    if device.type != "cuda":
+        _refuse(where, "tensors must be on a CUDA device")
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        status = call(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = call(*args, stream)
+    if status != MSA_OK:
+        raise MsaError(status, where)
+
+
+def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, context: float = 4096.0, slow: float = 1.0,
+                     fast: float = 32.0, device=None) -> torch.Tensor:
+    """Rotary frequencies (radians a token) as a float64 tensor [rot_dim / 2]; scaling is
+    "none", "linear", "base" or "parts" (msa_rope_frequencies in include/msa.h)."""
+    out = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.float64)
+    if scaling not in ROPE_SCALINGS:
+        _refuse("rope_frequencies", f"scaling {scaling!r}")
+    _check(lib.msa_rope_frequencies(int(rot_dim), float(base), ROPE_SCALINGS[scaling],
+                                    float(factor), float(context), float(slow), float(fast),
+                                    out.data_ptr() if out.numel() else None),
+           "msa_rope_frequencies")
+    return out.to(device or "cuda")
+
+
+def _rope_params(where, Q, K, Q_out, K_out, inv_freq, layout, mscale, inverse):
+    x = Q if Q is not None else K
+    if x is None:
+        _refuse(where, "Q and K are both None")
+    if layout not in ROPE_LAYOUTS:
+        _refuse(where, f"layout {layout!r}")
+    p = RopeParams()
+    p.q_stride = p.q_out_stride = p.k_stride = p.k_out_stride = 0
+    p.Hq = p.Hkv = 1
+    if Q is not None:
+        p.q_stride, p.Hq = _tokens(where, "Q", Q), Q.shape[1]
+        p.q_out_stride = _tokens(where, "Q_out", Q_out, Q)
+        if Q_out.shape != Q.shape:
+            _refuse(where, "Q_out: shape")
+    if K is not None:
+        p.k_stride, p.Hkv = _tokens(where, "K", K, x), K.shape[1]
+        if K.shape[0] != x.shape[0] or K.shape[2] != x.shape[2]:
+            _refuse(where, "K: shape")
+        if K_out is not None:
+            p.k_out_stride = _tokens(where, "K_out", K_out, K)
+            if K_out.shape != K.shape:
+                _refuse(where, "K_out: shape")
+    _dense(where, "inv_freq", inv_freq, torch.float64, x.device, (inv_freq.numel(),))
+    p.tokens, p.d, p.rot_dim = x.shape[0], x.shape[2], 2 * inv_freq.numel()
+    p.layout, p.inverse, p.dtype = ROPE_LAYOUTS[layout], int(bool(inverse)), _DTYPE_CODES[x.dtype]
+    p.mscale = mscale
+    return p, x
+
+
+def rope(Q, K, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0,
+         inverse: bool = False, Q_out=None, K_out=None):
+    """Rotary positions on Q [tokens, Hq, d] and K [tokens, Hkv, d] (either may be None);
+    positions [tokens] int32, inv_freq [rot_dim / 2] float64.  inverse=True applies the
+    transposed map (the gradient).  Q_out=Q, K_out=K turn in place.  Returns (Q_out, K_out)."""
+    if Q is not None and Q_out is None:
+        Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    if K is not None and K_out is None:
+        K_out = torch.empty(K.shape, dtype=K.dtype, device=K.device)
+    p, x = _rope_params("rope", Q, K, Q_out, K_out, inv_freq, layout, mscale, inverse)
+    pos = _dense("rope", "positions", positions, torch.int32, x.device, (p.tokens,))
+    if p.tokens:
+        _on_device("rope", x.device, lib.msa_rope, p, Q.data_ptr() if Q is not None else None,
+                   K.data_ptr() if K is not None else None, pos, inv_freq.data_ptr(),
+                   Q_out.data_ptr() if Q is not None else None,
+                   K_out.data_ptr() if K is not None else None)
+    return Q_out, K_out
+
+
+def _paged_args(where, B, K_cache, V_cache, seq_lens, block_table, dtype, device):
+    if K_cache.dim() != 4 or block_table.dim() != 2:
+        _refuse(where, "K_cache must be [num_pages, page_size, Hkv, d], block_table [B, max_pages]")
+    _dense(where, "K_cache", K_cache, dtype, device, K_cache.shape)
+    _dense(where, "V_cache", V_cache, dtype, device, K_cache.shape)
+    _dense(where, "seq_lens", seq_lens, torch.int32, device, (B,))
+    _dense(where, "block_table", block_table, torch.int32, device, (B, block_table.shape[1]))
+
+
+def rope_append_paged(Q, K, V, k_idx, cu_seqlens, seq_lens, block_table, inv_freq, K_cache,
+                      V_cache, k_idx_cache=None, *, layout: str = "half", mscale: float = 1.0,
+                      Q_out=None, workspace=None):
+    """New tokens enter the paged caches: rotary positions on Q and K, the turned K, V and
+    the index keys written to their pages (msa_rope_append_paged in include/msa.h).  Q, K and
+    V are packed [tokens, heads, d] (Q may be None), k_idx [tokens, d_idx] or None; seq_lens
+    counts the new tokens.  Returns (Q_out, workspace); the caches are updated in place."""
+    where = "rope_append_paged"
+    if Q is not None and Q_out is None:
+        Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    p, x = _rope_params(where, Q, K, Q_out, None, inv_freq, layout, mscale, False)
+    B = cu_seqlens.numel() - 1
+    _dense(where, "cu_seqlens", cu_seqlens, torch.int32, x.device, (B + 1,))
+    _paged_args(where, B, K_cache, V_cache, seq_lens, block_table, x.dtype, x.device)
+    v_stride = _tokens(where, "V", V, x)
+    if V.shape != K.shape or K_cache.shape[2:] != K.shape[1:]:
+        _refuse(where, "V or the caches: shape")
+    d_idx, idx, idx_cache = 0, None, None
+    if (k_idx is None) != (k_idx_cache is None):
+        _refuse(where, "k_idx and k_idx_cache go together")
+    if k_idx is not None:
+        d_idx = k_idx.shape[-1]
+        idx = _dense(where, "k_idx", k_idx, x.dtype, x.device, (p.tokens, d_idx))
+        idx_cache = _dense(where, "k_idx_cache", k_idx_cache, x.dtype, x.device,
+                           (*K_cache.shape[:2], d_idx))
+    if workspace is None:
+        workspace = torch.empty(256, dtype=torch.uint8, device=x.device)
+    if p.tokens == 0:
+        workspace[:256].zero_()
+        return Q_out, workspace
+    _on_device(where, x.device, lib.msa_rope_append_paged, p, B, cu_seqlens.data_ptr(),
+               seq_lens.data_ptr(), block_table.data_ptr(), K_cache.shape[1],
+               block_table.shape[1], K_cache.shape[0], Q.data_ptr() if Q is not None else None,
+               K.data_ptr(), V.data_ptr(), v_stride, idx, d_idx, inv_freq.data_ptr(),
+               Q_out.data_ptr() if Q is not None else None, K_cache.data_ptr(),
+               V_cache.data_ptr(), idx_cache, workspace.data_ptr(), workspace.numel())
+    return Q_out, workspace
+
+
+def _attn_call(where, paged, p, Q, out, lse, workspace, call, *args):
+    tokens, Hq, d = Q.shape
+    if out is None:
+        out = torch.empty((tokens, Hq, d), dtype=Q.dtype, device=Q.device)
+    else:
+        _dense(where, "out", out, Q.dtype, Q.device, Q.shape)
+    if lse is None:
+        lse = torch.empty((tokens, Hq), dtype=torch.float32, device=Q.device)
+    else:
+        _dense(where, "lse", lse, torch.float32, Q.device, (tokens, Hq))
+    p.tokens, p.Hq, p.d, p.dtype = tokens, Hq, d, _DTYPE_CODES[Q.dtype]
+    p.q_stride = _tokens(where, "Q", Q)
+    if workspace is None:
+        n = lib.msa_attn_workspace_size(p, paged)
+        if n == 0:
+            raise MsaError(2, f"{where}: sizes not supported")
+        workspace = torch.empty(n, dtype=torch.uint8, device=Q.device)
+    _on_device(where, Q.device, call, p, Q.data_ptr(), *args, out.data_ptr(), lse.data_ptr(),
+               workspace.data_ptr(), workspace.numel())
+    return out, lse, workspace
+
+
+def attn_packed(Q, K, V, cu_seqlens, cu_seqlens_k=None, *, scale: float = 0.0, out=None,
+                lse=None, workspace=None):
+    """Full causal attention of packed prompts: Q [tokens, Hq, d], K, V [key_tokens, Hkv, d],
+    cu_seqlens [B + 1] int32 (cu_seqlens_k for the keys where they differ; the queries are a
+    sequence's last positions).  Returns (O, lse, workspace).  Rows outside the sequences are
+    not written."""
+    where = "attn_packed"
+    p = AttnParams()
+    p.k_stride, p.v_stride = _tokens(where, "K", K, Q), _tokens(where, "V", V, Q)
+    if K.shape != V.shape or K.shape[2] != Q.shape[-1]:
+        _refuse(where, "K, V: shape")
+    p.B, p.key_tokens, p.Hkv, p.scale = cu_seqlens.numel() - 1, K.shape[0], K.shape[1], scale
+    cu_q = _dense(where, "cu_seqlens", cu_seqlens, torch.int32, Q.device, (p.B + 1,))
+    cu_k = cu_q
+    if cu_seqlens_k is not None:
+        cu_k = _dense(where, "cu_seqlens_k", cu_seqlens_k, torch.int32, Q.device, (p.B + 1,))
+    return _attn_call(where, 0, p, Q, out, lse, workspace, lib.msa_attn_packed, K.data_ptr(),
+                      V.data_ptr(), cu_q, cu_k)
+
+
+def attn_paged(Q, K_cache, V_cache, cu_seqlens, seq_lens, block_table, *, scale: float = 0.0,
+               out=None, lse=None, workspace=None):
+    """Full causal attention of new tokens Q [tokens, Hq, d] (packed by cu_seqlens [B + 1])
+    over a paged cache [num_pages, page_size, Hkv, d]; seq_lens [B] counts the cached keys, the
+    new tokens' own among them.  Returns (O, lse, workspace)."""
+    where = "attn_paged"
+    p = AttnParams()
+    p.B = cu_seqlens.numel() - 1
+    cu = _dense(where, "cu_seqlens", cu_seqlens, torch.int32, Q.device, (p.B + 1,))
+    _paged_args(where, p.B, K_cache, V_cache, seq_lens, block_table, Q.dtype, Q.device)
+    p.num_pages, p.page_size, p.Hkv = K_cache.shape[:3]
+    p.max_pages, p.scale = block_table.shape[1], scale
+    if K_cache.shape[3] != Q.shape[-1]:
+        _refuse(where, "K_cache: head dimension")
+    return _attn_call(where, 1, p, Q, out, lse, workspace, lib.msa_attn_paged,
+                      K_cache.data_ptr(), V_cache.data_ptr(), cu, seq_lens.data_ptr(),
+                      block_table.data_ptr())

@@ -1,0 +1,422 @@
+// full_attn.cu -- full causal attention of packed queries over packed or
+// paged keys: the plan kernel, the merge of rows whose keys were split, and
+// the CUDA-core kernel that serves fp32.
+//
+//   p(t) = L - T + t                  position of query t of a sequence
+//   O[t, h, :] = sum_{j <= p(t)} softmax(scale Q[t, h] . K[j, g])_j V[j, g, :]
+//   lse[t, h]  = log sum_{j <= p(t)} exp(scale Q[t, h] . K[j, g])
+//
+// with g = h / R.  The lengths are device data, so the cut of the work into
+// items is made on the device too: one CTA checks the offsets, lengths and
+// page ids, and writes each sequence's share of the item list.
+#include <math.h>
+
+#include <algorithm>
+
+#include "full_attn.cuh"
+
+namespace msa {
+namespace {
+
+// ---------------------------------------------------------------- plan
+
+constexpr int kPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kPlanThreads)
+full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *seqs,
+                 uint32_t *err) {
+    __shared__ int64_t warp_sum[32];
+    __shared__ int64_t total_tiles;
+    __shared__ int32_t base;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (tid < (int)(kErrorBytes / 4)) err[tid] = 0u;
+    // offsets: ascending, inside the arrays
+    bool bad = false;
+    for (int b = tid; b < s.B; b += kPlanThreads) {
+        const int32_t lo = q.cu_q[b], hi = q.cu_q[b + 1];
+        bad |= lo < 0 || hi < lo || hi > s.tokens;
+        if (!s.paged) {
+            const int32_t kl = q.cu_k[b], kh = q.cu_k[b + 1];
+            bad |= kl < 0 || kh < kl || kh > s.key_tokens;
+        }
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) {
+            record_error(err, MSA_ERR_BAD_OFFSETS, 3);
+            plan->items = 0;
+            plan->invalid = 1;
+        }
+        return;
+    }
+    // lengths; a paged sequence with a length outside [T, capacity] or a bad
+    // page id gets L = 0
+    for (int b = tid; b < s.B; b += kPlanThreads) {
+        const int32_t q0 = q.cu_q[b], T = q.cu_q[b + 1] - q0;
+        int32_t L, k0 = 0;
+        if (s.paged) {
+            L = q.seq_lens[b];
+            if (L < T || (int64_t)L > (int64_t)s.max_pages * s.page_size) {
+                L = 0;
+                record_error(err, MSA_ERR_BAD_PAGE_TABLE, 3);
+            }
+        } else {
+            k0 = q.cu_k[b];
+            L = q.cu_k[b + 1] - k0;
+        }
+        seqs[b].q0 = q0;
+        seqs[b].T = T;
+        seqs[b].L = L;
+        seqs[b].k0 = k0;
+    }
+    __syncthreads();
+    if (s.paged) {
+        // wps warps a sequence (more than one where there are few sequences)
+        const int wps = max(1, 32 / s.B), at_once = 32 / wps;
+        for (int b = warp / wps; b < s.B && warp < at_once * wps; b += at_once) {
+            const int n = (int)(((int64_t)seqs[b].L + s.page_size - 1) / s.page_size);
+            const int32_t *row = q.block_table + (int64_t)b * s.max_pages;
+            bool wrong = false;
+            for (int i = (warp % wps) * 32 + lane; i < n; i += wps * 32) {
+                const int32_t pg = row[i];
+                wrong |= pg < 0 || pg >= s.num_pages;
+            }
+            if (__any_sync(0xffffffffu, wrong) && lane == 0) {
+                record_error(err, MSA_ERR_BAD_PAGE_TABLE, 3);
+                seqs[b].k0 = -1;                   // marked; L is still being read
+            }
+        }
+        __syncthreads();
+        for (int b = tid; b < s.B; b += kPlanThreads)
+            if (seqs[b].k0 < 0) {
+                seqs[b].L = 0;
+                seqs[b].k0 = 0;
+            }
+    }
+    // key tiles of all units, for the length of a key run
+    int64_t mine = 0;
+    for (int b = tid; b < s.B; b += kPlanThreads) {
+        const int units = (seqs[b].T + c.unit_tokens - 1) / c.unit_tokens;
+        mine += (int64_t)units * s.Hkv * ((seqs[b].L + kFullKeys - 1) / kFullKeys);
+    }
+    for (int off = 16; off > 0; off /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+    if (lane == 0) warp_sum[warp] = mine;
+    if (tid == 0) base = 0;
+    __syncthreads();
+    if (tid == 0) {
+        int64_t n = 0;
+        for (int w = 0; w < 32; ++w) n += warp_sum[w];
+        total_tiles = n;
+    }
+    __syncthreads();
+    const int64_t run = c.split > 0 ? max((int64_t)c.min_tiles, (total_tiles + c.split - 1) / c.split)
+                                    : (int64_t)1 << 30;
+    // items of each sequence, and their running sum
+    for (int b0 = 0; b0 < s.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int n = 0;
+        if (b < s.B) {
+            const int tiles = (seqs[b].L + kFullKeys - 1) / kFullKeys;
+            const int units = (seqs[b].T + c.unit_tokens - 1) / c.unit_tokens;
+            int parts = (int)min((int64_t)max(1, c.max_parts), (tiles + run - 1) / run);
+            parts = max(parts, 1);
+            const int per = max(1, (tiles + parts - 1) / parts);
+            seqs[b].units = units;
+            seqs[b].parts = parts;
+            seqs[b].tiles = per;
+            n = units * parts * s.Hkv;
+        }
+        int sum = n;                               // inclusive over the warp, then the CTA
+        for (int off = 1; off < 32; off *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += o;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        int before = base;
+        for (int w = 0; w < warp; ++w) before += (int)warp_sum[w];
+        if (b < s.B) seqs[b].first_item = before + sum - n;
+        __syncthreads();
+        if (tid == kPlanThreads - 1) base = before + sum;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        plan->items = base;
+        plan->invalid = 0;
+    }
+}
+
+// ---------------------------------------------------------------- merge
+
+constexpr int kMergeThreads = 256;
+
+// Rows of a token whose keys were split: weights exp(lse_i - max lse), summed
+// in the order of the parts.  One CTA a token, one warp a head at a time,
+// lane l channels 4 l .. 4 l + 3.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads)
+full_combine_kernel(FullShape s, FullSeqs q, FullCut c, const FullPlan *plan, const FullSeq *seqs,
+                    const float *__restrict__ part_o, const float *__restrict__ part_lse,
+                    __nv_bfloat16 *__restrict__ O, float *__restrict__ lse) {
+    if (plan->invalid) return;
+    const int64_t n = blockIdx.x;
+    int b = 0;
+    for (int b0 = 0; b0 < s.B; b0 += kMergeThreads)
+        b += __syncthreads_count(b0 + threadIdx.x < s.B && q.cu_q[b0 + threadIdx.x + 1] <= n);
+    if (b >= s.B) return;
+    const FullSeq sq = seqs[b];
+    if (n < sq.q0) return;
+    const int parts = full_row_parts(sq, c, (int)(n - sq.q0));
+    if (parts == 0) return;
+    constexpr int kPer = D / 32;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int h = warp; h < s.Hq; h += kMergeThreads / 32) {
+        const int64_t row = n * s.Hq + h, step = s.tokens * s.Hq;
+        float m = -INFINITY;
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, part_lse[row + i * step]);
+        for (int off = 16; off > 0; off /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        float sum = 0.f, acc[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+        for (int i = 0; i < parts; ++i) {
+            const float l = part_lse[row + i * step];
+            if (l == -INFINITY) continue;          // no key of this part: nothing was stored
+            const float w = expf(l - m);
+            sum += w;
+            const float *src = part_o + (row + i * step) * D + lane * kPer;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) acc[k] = fmaf(w, src[k], acc[k]);
+        }
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            O[row * D + lane * kPer + k] = __float2bfloat16_rn(acc[k] * inv);
+        if (lane == 0) lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
+    }
+}
+
+// ---------------------------------------------------------------- CUDA cores
+
+constexpr int kSimtThreads = 128;
+constexpr int kSimtRows = 64;              // rows = (token, head of the group) pairs
+constexpr int kSimtKeys = 32;
+
+// A CTA takes an item's rows: q in shared memory, keys 32 at a time.
+// Scores: thread (y, x) owns rows 4 y .. 4 y + 3 and keys x, x + 8, x + 16,
+// x + 24; softmax: two threads a row; values: rows 4 y .. and channels
+// 4 x + 32 k ...  A score costs d multiply-adds from shared memory and so
+// does a weight: 64 of them for each eight 16-byte reads.
+template <typename T, int D>
+__global__ void __launch_bounds__(kSimtThreads)
+full_simt_kernel(FullShape s, FullSeqs sq, FullCut c, const FullPlan *plan, const FullSeq *seqs,
+                 const T *__restrict__ Q, const T *__restrict__ K, const T *__restrict__ V,
+                 T *__restrict__ O, float *__restrict__ lse) {
+    constexpr int kLd = D + 4;
+    extern __shared__ __align__(16) float sm[];
+    float *qs = sm;                                        // [64][D + 4]
+    float *ks = qs + kSimtRows * kLd;                      // [32][D + 4]
+    float *vs = ks + kSimtKeys * kLd;                      // [32][D]
+    float *ps = vs + kSimtKeys * D;                        // [64][36]
+    float *alpha = ps + kSimtRows * 36;                    // [64]
+    float *inv_l = alpha + kSimtRows;                      // [64]
+    const int tid = threadIdx.x, lane = tid % 32;
+    const int y = tid / 8, x = tid % 8;
+    const int items = plan->items;
+    int b = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        b = full_find_seq(seqs, s.B, b, item, lane);
+        const FullSeq q = seqs[b];
+        const int local = item - q.first_item;
+        const int g = local / q.units, u = q.units - 1 - local % q.units;
+        const int t0 = u * c.unit_tokens, nt = min(c.unit_tokens, q.T - t0);
+        const int rows = nt * s.R;
+        const int pos0 = q.L - q.T + t0;                   // position of the first token
+        const int last = pos0 + nt;                        // no row sees key `last` or later
+        for (int i = tid; i < kSimtRows * (D / 4); i += kSimtThreads) {
+            const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows) {
+                const T *p = Q + (int64_t)(q.q0 + t0 + r / s.R) * s.q_stride +
+                             (int64_t)(g * s.R + r % s.R) * D + ch;
+                v = make_float4(to_f32(p[0]), to_f32(p[1]), to_f32(p[2]), to_f32(p[3]));
+            }
+            *(float4 *)(qs + r * kLd + ch) = v;
+        }
+        float acc[4][D / 8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) acc[i][k] = 0.f;
+        float m = -INFINITY, l = 0.f;                      // of row tid / 2
+        for (int j0 = 0; j0 < last; j0 += kSimtKeys) {
+            __syncthreads();
+            for (int i = tid; i < kSimtKeys * (D / 4); i += kSimtThreads) {
+                const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
+                float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+                const int j = j0 + r;
+                if (j < last) {
+                    int64_t kr = (int64_t)q.k0 + j;
+                    bool in = true;
+                    if (s.paged) {
+                        const int pg = sq.block_table[(int64_t)b * s.max_pages + j / s.page_size];
+                        kr = (int64_t)pg * s.page_size + j % s.page_size;
+                        in = MSA_IN_BOUNDS(kr, (int64_t)s.num_pages * s.page_size);
+                    }
+                    if (in) {
+                        const T *kp = K + kr * s.k_stride + (int64_t)g * D + ch;
+                        const T *vp = V + kr * s.v_stride + (int64_t)g * D + ch;
+                        kv = make_float4(to_f32(kp[0]), to_f32(kp[1]), to_f32(kp[2]), to_f32(kp[3]));
+                        vv = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
+                    }
+                }
+                *(float4 *)(ks + r * kLd + ch) = kv;
+                *(float4 *)(vs + r * D + ch) = vv;
+            }
+            __syncthreads();
+            float sc[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sc[i][k] = 0.f;
+#pragma unroll 4
+            for (int ch = 0; ch < D; ch += 4) {
+                float4 qv[4], kv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qv[i] = *(const float4 *)(qs + (4 * y + i) * kLd + ch);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) kv[k] = *(const float4 *)(ks + (x + 8 * k) * kLd + ch);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sc[i][k] = fmaf(qv[i].x, kv[k].x, fmaf(qv[i].y, kv[k].y,
+                                   fmaf(qv[i].z, kv[k].z, fmaf(qv[i].w, kv[k].w, sc[i][k]))));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * y + i, p = pos0 + r / s.R;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    ps[r * 36 + x + 8 * k] = j0 + x + 8 * k <= p ? sc[i][k] * s.scale : -INFINITY;
+            }
+            __syncthreads();
+            {
+                float *pr = ps + (tid / 2) * 36 + (tid % 2) * 16;
+                float top = m;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) top = fmaxf(top, pr[k]);
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                const float at = top == -INFINITY ? 0.f : top;
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float w = expf(pr[k] - at);
+                    pr[k] = w;
+                    sum += w;
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                const float a = m == -INFINITY ? 0.f : expf(m - at);
+                l = l * a + sum;
+                m = top;
+                if (tid % 2 == 0) alpha[tid / 2] = a;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = alpha[4 * y + i];
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) acc[i][k] *= a;
+            }
+            // a tile that some row sees only in part: that row leaves the
+            // later values out (they may be infinite or NaN)
+            const bool whole = j0 + kSimtKeys <= pos0 + 1;
+            for (int j = 0; j < kSimtKeys; ++j) {
+                float4 v[D / 32];
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) v[k] = *(const float4 *)(vs + j * D + 4 * x + 32 * k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (!whole && j0 + j > pos0 + (4 * y + i) / s.R) continue;
+                    const float w = ps[(4 * y + i) * 36 + j];
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        acc[i][4 * k] = fmaf(w, v[k].x, acc[i][4 * k]);
+                        acc[i][4 * k + 1] = fmaf(w, v[k].y, acc[i][4 * k + 1]);
+                        acc[i][4 * k + 2] = fmaf(w, v[k].z, acc[i][4 * k + 2]);
+                        acc[i][4 * k + 3] = fmaf(w, v[k].w, acc[i][4 * k + 3]);
+                    }
+                }
+            }
+        }
+        if (tid % 2 == 0) {
+            const int r = tid / 2;
+            inv_l[r] = l == 0.f ? 0.f : 1.f / l;
+            if (r < rows)
+                lse[(int64_t)(q.q0 + t0 + r / s.R) * s.Hq + g * s.R + r % s.R] =
+                    l == 0.f ? -INFINITY : m + logf(l);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * y + i;
+            if (r >= rows) continue;
+            T *dst = O + ((int64_t)(q.q0 + t0 + r / s.R) * s.Hq + g * s.R + r % s.R) * D;
+            const float inv = inv_l[r];
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    dst[4 * x + 32 * k + e] = from_f32<T>(acc[i][4 * k + e] * inv);
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_simt_t(const FullShape &s, const FullSeqs &q, const FullCut &c,
+                          const FullPlan *plan, const FullSeq *seqs, const void *Q, const void *K,
+                          const void *V, void *O, float *lse, cudaStream_t st) {
+    const size_t smem = sizeof(float) * ((size_t)(kSimtRows + kSimtKeys) * (D + 4) + kSimtKeys * D +
+                                         kSimtRows * 36 + 2 * kSimtRows);
+    auto k = full_simt_kernel<T, D>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (s.tokens / c.unit_tokens + s.B) * s.Hkv;
+    k<<<(unsigned)std::min<int64_t>(most, 148 * 3 * 16), kSimtThreads, smem, st>>>(
+        s, q, c, plan, seqs, (const T *)Q, (const T *)K, (const T *)V, (T *)O, lse);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_full_plan(const FullShape &s, const FullSeqs &q, const FullCut &c,
+                             FullPlan *plan, FullSeq *seqs, uint32_t *err, cudaStream_t st) {
+    full_plan_kernel<<<1, kPlanThreads, 0, st>>>(s, q, c, plan, seqs, err);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_full_combine(const FullShape &s, const FullSeqs &q, const FullCut &c,
+                                const FullPlan *plan, const FullSeq *seqs, const float *part_o,
+                                const float *part_lse, void *O, float *lse, cudaStream_t st) {
+    auto k = s.d == 64 ? full_combine_kernel<64> : full_combine_kernel<128>;
+    k<<<(unsigned)s.tokens, kMergeThreads, 0, st>>>(s, q, c, plan, seqs, part_o, part_lse,
+                                                    (__nv_bfloat16 *)O, lse);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+FullCut full_simt_cut(const FullShape &s) { return FullCut{kSimtRows / s.R, 0, 0, 1, 1}; }
+
+cudaError_t launch_full_simt(const FullShape &s, const FullSeqs &q, const FullCut &c,
+                             const FullPlan *plan, const FullSeq *seqs, const void *Q,
+                             const void *K, const void *V, void *O, float *lse, cudaStream_t st) {
+    if (s.dtype == MSA_BF16)
+        return s.d == 64
+                   ? launch_simt_t<__nv_bfloat16, 64>(s, q, c, plan, seqs, Q, K, V, O, lse, st)
+                   : launch_simt_t<__nv_bfloat16, 128>(s, q, c, plan, seqs, Q, K, V, O, lse, st);
+    return s.d == 64 ? launch_simt_t<float, 64>(s, q, c, plan, seqs, Q, K, V, O, lse, st)
+                     : launch_simt_t<float, 128>(s, q, c, plan, seqs, Q, K, V, O, lse, st);
+}
+
+}  // namespace msa

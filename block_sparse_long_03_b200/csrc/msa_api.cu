@@ -263,6 +263,7 @@ const char *msa_status_string(msa_status_t status) {
         case MSA_ERR_WORKSPACE: return "MSA_ERR_WORKSPACE: workspace missing, misaligned or too small";
         case MSA_ERR_BAD_BLOCK_IDS: return "MSA_ERR_BAD_BLOCK_IDS: caller block ids out of range, not causal or repeated";
         case MSA_ERR_BAD_PAGE_TABLE: return "MSA_ERR_BAD_PAGE_TABLE: a sequence length or page id of a paged call is out of range";
+        case MSA_ERR_BAD_OFFSETS: return "MSA_ERR_BAD_OFFSETS: sequence offsets of a packed call descend or leave the arrays";
     }
     return "unknown msa_status_t";
 }

@@ -197,6 +197,28 @@ cudaError_t launch_fine_scores(const Shape &s, const void *q_idx, const void *k_
 // otherwise 0 (the sequence does no work) with MSA_ERR_BAD_PAGE_TABLE recorded.
 cudaError_t launch_paged_check(const Shape &s, const int32_t *lens, const KeyRows &rows,
                                int32_t *lens_ok, uint32_t *err, cudaStream_t st);
+// Rotary positions (rope.cu).  Q with Hq = 0 or K with Hkv = 0: none.
+struct RopeArgs {
+    const void *Q, *K;
+    void *Q_out, *K_out;                 // K_out: the key cache for the append
+    const int32_t *positions;            // not read by the append
+    const double *inv_freq;
+    int64_t tokens, q_stride, k_stride, qo_stride, ko_stride;
+    int Hq, Hkv, d, rot, inverse;
+    float mscale;
+};
+struct AppendArgs {
+    const int32_t *cu_seqlens, *seq_lens, *block_table;
+    const void *V, *k_idx;
+    void *V_cache, *k_idx_cache;
+    int64_t v_stride;
+    int B, page_size, max_pages, num_pages, d_idx;
+    uint32_t *err;
+};
+cudaError_t launch_rope(const RopeArgs &a, int dtype, bool side, cudaStream_t st);
+cudaError_t launch_rope_append(const RopeArgs &a, const AppendArgs &c, int dtype, bool side,
+                               cudaStream_t st);
+
 cudaError_t launch_attn_simt(const Shape &s, const void *Q, const void *K, const void *V,
                              const int32_t *ids, void *O, float *lse, uint32_t *err,
                              cudaStream_t st, float *mass = nullptr);

@@ -60,7 +60,8 @@ typedef enum {
     MSA_ERR_DEVICE_TIMEOUT = 4,  /* a bounded device wait gave up             */
     MSA_ERR_WORKSPACE = 5,       /* workspace missing or too small            */
     MSA_ERR_BAD_BLOCK_IDS = 6,   /* caller ids out of range / not causal      */
-    MSA_ERR_BAD_PAGE_TABLE = 7   /* paged call: a length or page id invalid   */
+    MSA_ERR_BAD_PAGE_TABLE = 7,  /* paged call: a length or page id invalid   */
+    MSA_ERR_BAD_OFFSETS = 8      /* packed call: sequence offsets invalid     */
 } msa_status_t;
 
 typedef enum { MSA_F32 = 0, MSA_BF16 = 1 } msa_dtype_t;
@@ -389,6 +390,172 @@ MSA_EXPORT msa_status_t msa_decode_paged(const msa_params_t *params, const int32
                                          const void *K_cache, const void *V_cache,
                                          int32_t *block_ids, void *O, float *lse,
                                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Serving operators: rotary positions, the write of new tokens into the
+ * paged caches, and full (not block-sparse) causal attention.  The source
+ * pages name none of them; they are what a program around the calls above
+ * needs before and next to them: positions on Q and K, something that fills
+ * the caches msa_decode_paged reads, and attention for the layers that keep
+ * every key.  Tokens are PACKED here: the tokens of all sequences lie one
+ * after another, and cu_seqlens [B + 1] (int32, ascending) says that
+ * sequence b's are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  Rows before
+ * cu_seqlens[0] and from cu_seqlens[B] on belong to no sequence: they are not
+ * read and their outputs are left as they were.  A sequence may have no
+ * tokens.  Strides are in elements, from one token to the next (so that Q, K
+ * and V may be slices of one projection's output); 0 means dense; a token's
+ * heads are dense.  They must keep every token 16-byte aligned.
+ * --------------------------------------------------------------------- */
+
+/* How a rotated head's channels are paired: channel i with i + rot_dim / 2,
+ * or 2 i with 2 i + 1. */
+#define MSA_ROPE_HALF 0
+#define MSA_ROPE_INTERLEAVED 1
+
+/* Frequencies' scaling for contexts `factor` times the trained one. */
+#define MSA_ROPE_SCALE_NONE 0
+#define MSA_ROPE_SCALE_LINEAR 1   /* every frequency / factor                */
+#define MSA_ROPE_SCALE_BASE 2     /* base * factor^(rot_dim / (rot_dim - 2)) */
+#define MSA_ROPE_SCALE_PARTS 3    /* slow frequencies only, see below        */
+
+/*
+ * Rotary frequencies, on the host: inv_freq[i] = base^(-2 i / rot_dim)
+ * radians a token, i < rot_dim / 2, scaled as `scaling` says.
+ * MSA_ROPE_SCALE_PARTS: a frequency that makes r = context * inv_freq / (2 pi)
+ * turns in the trained context is kept where r >= fast, divided by factor
+ * where r <= slow, and between them is the mix
+ *   w * inv_freq + (1 - w) * inv_freq / factor,  w = (r - slow) / (fast - slow).
+ * context, slow and fast are read for MSA_ROPE_SCALE_PARTS only, factor for
+ * every scaling but NONE.  rot_dim even, >= 2 (>= 4 for BASE); base > 1;
+ * factor > 0; context > 0; fast > slow >= 0; otherwise MSA_ERR_INVALID_ARG.
+ */
+MSA_EXPORT msa_status_t msa_rope_frequencies(int32_t rot_dim, double base, int32_t scaling,
+                                             double factor, double context, double slow,
+                                             double fast, double *inv_freq);
+
+typedef struct {
+    int64_t tokens;      /* rows of Q and K                                      */
+    int64_t q_stride, k_stride;           /* of the inputs                        */
+    int64_t q_out_stride, k_out_stride;   /* of the outputs                       */
+    int32_t Hq, Hkv;     /* heads of Q and of K, at most 1024 each               */
+    int32_t d;           /* head dimension: a multiple of 16, <= 256             */
+    int32_t rot_dim;     /* channels turned, the first ones of each head: a      */
+                         /* multiple of 16, <= d                                 */
+    int32_t layout;      /* MSA_ROPE_HALF or MSA_ROPE_INTERLEAVED                */
+    int32_t inverse;     /* 0: turn; 1: the transposed turn (the gradient)       */
+    int32_t dtype;       /* msa_dtype_t                                          */
+    float mscale;        /* factor on the turned channels (1: none)              */
+} msa_rope_params_t;
+
+/*
+ * Rotary positions on Q and K.  For a pair (x_a, x_b) of channels with
+ * frequency theta_i of a token at position p:
+ *   y_a = mscale * (x_a cos(p theta_i) - x_b sin(p theta_i))
+ *   y_b = mscale * (x_b cos(p theta_i) + x_a sin(p theta_i))
+ * and the other channels are copied.  inverse = 1 negates the sine: the
+ * transposed map, which takes the gradient of the outputs to that of the
+ * inputs.  The products are fp32, rounded once to dtype; the angles are
+ * formed in fp64, so that far positions (2^20 and beyond) lose nothing.
+ *
+ * Q [tokens, Hq, d], K [tokens, Hkv, d] (dtype, read); positions [tokens]
+ * int32 (read; any value, negative ones too); inv_freq [rot_dim / 2] FLOAT64
+ * (device, read); Q_out, K_out (written).  An output may be its input
+ * (with the same stride); other overlaps are not allowed.  Either pair (Q,
+ * Q_out) or (K, K_out) may be NULL, NULL.  tokens may be 0.
+ */
+MSA_EXPORT msa_status_t msa_rope(const msa_rope_params_t *params, const void *Q, const void *K,
+                                 const int32_t *positions, const double *inv_freq, void *Q_out,
+                                 void *K_out, void *stream);
+
+/*
+ * New tokens enter the paged caches: rotary positions as msa_rope
+ * (inverse = 0) on Q and K, with the turned K, V and the index keys written
+ * to the rows msa_decode_paged and msa_attn_paged read.  Sequence b has
+ * L_b = seq_lens[b] keys once its T_b = cu_seqlens[b + 1] - cu_seqlens[b] new
+ * tokens are in; new token t has position p = L_b - T_b + t and goes to row
+ * p % page_size of page block_table[b, p / page_size].
+ *
+ * params: as msa_rope; k_out_stride is not read (the caches are dense).
+ * V [tokens, Hkv, d] with v_stride; k_idx [tokens, d_idx] dense, written as
+ * it is (turn it with msa_rope first where the model does), d_idx a multiple
+ * of 16, <= 128, or k_idx = k_idx_cache = NULL.  Q = Q_out = NULL: keys only.
+ * seq_lens, block_table, page_size, max_pages, num_pages and the caches: as
+ * msa_decode_paged.  Two tokens must not have the same cache row.
+ * workspace: at least 256 bytes, 256-byte aligned: the device error word.
+ *
+ * Lengths and page ids are checked on the device: a token whose sequence
+ * has L_b < T_b, L_b > max_pages * page_size or unusable offsets, or whose
+ * page id is outside [0, num_pages), is skipped (nothing of it is written,
+ * Q_out neither) and the error word records MSA_ERR_BAD_PAGE_TABLE.
+ */
+MSA_EXPORT msa_status_t msa_rope_append_paged(
+    const msa_rope_params_t *params, int32_t B, const int32_t *cu_seqlens,
+    const int32_t *seq_lens, const int32_t *block_table, int32_t page_size, int32_t max_pages,
+    int32_t num_pages, const void *Q, const void *K, const void *V, int64_t v_stride,
+    const void *k_idx, int32_t d_idx, const double *inv_freq, void *Q_out, void *K_cache,
+    void *V_cache, void *k_idx_cache, void *workspace, size_t workspace_bytes, void *stream);
+
+typedef struct {
+    int64_t tokens;      /* rows of Q, O and lse, < 2^31                         */
+    int64_t key_tokens;  /* rows of packed K and V (paged calls: not read)       */
+    int64_t q_stride, k_stride, v_stride;   /* paged calls read q_stride only    */
+    int32_t B;           /* sequences                                            */
+    int32_t Hq, Hkv;     /* heads; Hq % Hkv == 0, Hq / Hkv <= 64                 */
+    int32_t d;           /* head dimension: 64 or 128                            */
+    int32_t dtype;       /* msa_dtype_t                                          */
+    float scale;         /* softmax scale; <= 0 selects 1/sqrt(d)                */
+    int32_t page_size, max_pages, num_pages;   /* paged calls only               */
+} msa_attn_params_t;
+
+/* Workspace bytes of msa_attn_packed (paged = 0) or msa_attn_paged
+ * (paged = 1); 0 for invalid or unsupported sizes. */
+MSA_EXPORT size_t msa_attn_workspace_size(const msa_attn_params_t *params, int paged);
+
+/*
+ * Full causal attention of packed prompts.  Query t of sequence b, of
+ * T_b queries and L_b keys, sits at position p(t) = L_b - T_b + t:
+ *   s_j = scale * sum_c Q[t, h, c] * K[j, g, c],   j <= p(t),  g = h / (Hq / Hkv)
+ *   O[t, h, :] = sum_j softmax(s)_j V[j, g, :]
+ *   lse[t, h]  = log(sum_j exp(s_j))
+ * over the sequence's own keys.  A query with no key (p(t) < 0) gets O = 0
+ * and lse = -infinity.  Keys and values that a query does not attend have no
+ * influence on it, infinities and NaN included.  bf16: fp32 scores, softmax
+ * and sums; the weights are rounded to bf16 for the product with V.
+ *
+ * Q [tokens, Hq, d], K, V [key_tokens, Hkv, d] (dtype, read); cu_seqlens_q,
+ * cu_seqlens_k [B + 1] int32 (device, read; the same array for plain
+ * prompts); O [tokens, Hq, d] dense (dtype, written), lse [tokens, Hq]
+ * float32 (written).  workspace: msa_attn_workspace_size(params, 0) bytes,
+ * 256-byte aligned, used by one call at a time; first 256 bytes: the device
+ * error word.
+ *
+ * Offsets that descend or leave the arrays are found on the device: no row
+ * is written then, and the error word records MSA_ERR_BAD_OFFSETS.
+ */
+MSA_EXPORT msa_status_t msa_attn_packed(const msa_attn_params_t *params, const void *Q,
+                                        const void *K, const void *V,
+                                        const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                        void *O, float *lse, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/*
+ * The same attention of new tokens over a paged cache: T_b queries (one
+ * token, a chunk, or none) of sequence b over its L_b = seq_lens[b] cached
+ * keys, the new tokens' own among them (msa_rope_append_paged writes them).
+ * seq_lens, block_table and the caches are those of msa_decode_paged, with a
+ * page_size that is a multiple of 8 for bf16.  Rows of a page behind a
+ * sequence's length are never used.
+ *
+ * A sequence with L_b < T_b, L_b > max_pages * page_size or a page id outside
+ * [0, num_pages) among its first ceil(L_b / page_size) is skipped: its O is
+ * 0, its lse -infinity, and the error word records MSA_ERR_BAD_PAGE_TABLE.
+ * Bad offsets: as msa_attn_packed.
+ */
+MSA_EXPORT msa_status_t msa_attn_paged(const msa_attn_params_t *params, const void *Q,
+                                       const void *K_cache, const void *V_cache,
+                                       const int32_t *cu_seqlens, const int32_t *seq_lens,
+                                       const int32_t *block_table, void *O, float *lse,
+                                       void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Diagnostics: the query pieces a call splits its work into, computed on the
