@@ -45,6 +45,7 @@ full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *se
             record_error(err, MSA_ERR_BAD_OFFSETS, 3);
             plan->items = 0;
             plan->invalid = 1;
+            plan->next = 0;
         }
         return;
     }
@@ -142,6 +143,7 @@ full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *se
     if (tid == 0) {
         plan->items = base;
         plan->invalid = 0;
+        plan->next = 0;
     }
 }
 

@@ -39,6 +39,7 @@ struct FullSeq {
 // (late queries, which see the most keys, first).
 struct FullPlan {
     int32_t items, invalid;              // invalid: the offsets are unusable, no row is written
+    int32_t next;                        // items handed out beyond each CTA's first
 };
 constexpr size_t kPlanBytes = 256;
 
@@ -75,6 +76,13 @@ FullCut full_simt_cut(const FullShape &s);
 cudaError_t launch_full_simt(const FullShape &s, const FullSeqs &q, const FullCut &c,
                              const FullPlan *plan, const FullSeq *seqs, const void *Q,
                              const void *K, const void *V, void *O, float *lse, cudaStream_t st);
+
+// Tensor-core kernel (bf16, full_attn_tc.cu).
+FullCut full_tc_cut(const FullShape &s);
+cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut &c,
+                           const FullPlan *plan, const FullSeq *seqs, const void *Q,
+                           const void *K, const void *V, void *O, float *lse, float *part_o,
+                           float *part_lse, uint32_t *err, cudaStream_t st);
 
 // The sequence that item `i` belongs to, searched from sequence b on (items
 // are visited in ascending order), by one warp.

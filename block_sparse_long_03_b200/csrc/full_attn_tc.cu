@@ -1,0 +1,739 @@
+// full_attn_tc.cu -- full causal attention on the tensor cores (bf16), over
+// packed or paged keys, from one query token to whole prompts.
+//
+//   O = softmax(scale Q K^T + causal) V,   lse = log sum exp(scale Q K^T)
+//
+// A row tile is 128 (token, head of the KV group) rows: 128 / R tokens with
+// their R query heads, so that K and V are read once for the group.  A CTA
+// holds two of them in flight (streams 0 and 1), each with its own softmax
+// warpgroup, so that the tensor cores work on one while the other is in its
+// softmax.  A unit of work is two row tiles of consecutive tokens against the
+// same keys; one of at most 128 / R tokens (decode, ends of prompts) is a
+// single row tile whose key run the two streams share half and half.
+//
+//   S = Q K^T      tcgen05, operands from shared memory, fp32 in TMEM
+//   P = 2^(scale log2(e) (S - m))    in registers, bf16 over S in TMEM
+//   O += P V       tcgen05, P from TMEM, O (fp32) in TMEM
+//
+// The running maximum m a row's P is taken against moves only when a tile's
+// maximum passes it by more than 2^8: P stays below 2^8 (the same relative
+// rounding in bf16, far from fp32's range) and O is rarely rescaled.  The
+// fp32 row sum is of the unrounded P.  TMEM: S/P of the streams in columns
+// 0 and 128, O in 256 and 384.
+#include <math.h>
+
+#include <algorithm>
+
+#include "full_attn.cuh"
+#include "tc.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 384;            // loads + MMA + value check, two softmax warpgroups
+constexpr int kRows = 128;               // rows of a row tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMaxLag = 8.f;           // log2 of how far P may pass 1
+constexpr int kRegsLoad = 88, kRegsSoftmax = 208;
+static_assert(kRegsLoad + 2 * kRegsSoftmax <= 3 * 168, "register budgets exceed the launch's");
+
+template <int D> constexpr int ring_slots() { return D == 128 ? 5 : 10; }
+template <int D> constexpr size_t tc_smem() {
+    return 1024 + (2 + (size_t)ring_slots<D>()) * 128 * D * 2 + 1024;
+}
+
+struct TcArgs {
+    FullShape s;
+    FullSeqs q;
+    FullCut c;
+    const FullPlan *plan;
+    const FullSeq *seqs;
+    int *next;                           // the next item to take
+    const __nv_bfloat16 *V;
+    __nv_bfloat16 *O;
+    float *lse, *part_o, *part_lse;
+    uint32_t *err;
+    int box;                             // key rows of one TMA box
+    float scale_log2;
+};
+
+// A work item as the loading warp hands it to the others.
+struct Item {
+    int valid, b, g, q0;                 // q0: row of Q of the unit's first token
+    int nt, pos0, k0, pair;              // tokens; position of the first; packed key row 0
+    int a0, a1, n0, n1;                  // each stream's first key tile and their number
+    int part, parts, pad0, pad1;         // key run, and how many the rows' results come in
+};
+
+__device__ __forceinline__ int stream_a(const Item &w, int s) { return s ? w.a1 : w.a0; }
+__device__ __forceinline__ int stream_n(const Item &w, int s) { return s ? w.n1 : w.n0; }
+// The streams read the same key tiles (a pair of row tiles, or one stream idle).
+__device__ __forceinline__ bool shared_keys(const Item &w) { return w.pair || w.n1 == 0; }
+// Some row of the unit does not attend all of key tile t.
+__device__ __forceinline__ bool edge_tile(const Item &w, int t) {
+    return (t + 1) * kFullKeys > w.pos0 + 1;
+}
+
+__device__ __forceinline__ Item make_item(const TcArgs &a, const FullSeq &q, int b, int item) {
+    Item w;
+    const int local = item - q.first_item, per = q.units * q.parts;
+    const int r = local % per;
+    const int u = q.units - 1 - r % q.units;
+    w.valid = 1;
+    w.b = b;
+    w.g = local / per;
+    w.part = r / q.units;
+    const int t0 = u * a.c.unit_tokens;
+    w.nt = min(a.c.unit_tokens, q.T - t0);
+    w.q0 = q.q0 + t0;
+    w.pos0 = q.L - q.T + t0;
+    w.k0 = q.k0;
+    w.pair = w.nt > a.c.half_tokens;
+    w.parts = full_row_parts(q, a.c, t0);
+    const int lo = w.part * q.tiles;
+    auto run = [&](int tokens) {         // key tiles of this part that the first tokens see
+        const int seen = (max(0, w.pos0 + tokens) + kFullKeys - 1) / kFullKeys;
+        return max(0, min(seen, lo + q.tiles) - lo);
+    };
+    const int n = run(w.nt);
+    w.a0 = w.a1 = lo;
+    if (w.pair) {
+        w.n0 = run(a.c.half_tokens);
+        w.n1 = n;
+    } else if (a.c.max_parts > 1) {
+        w.n0 = (n + 1) / 2;
+        w.n1 = n - w.n0;
+        w.a1 = lo + w.n0;
+        w.part *= 2;
+    } else {
+        w.n0 = n;
+        w.n1 = 0;
+    }
+    return w;
+}
+
+struct Bars {
+    // a slot's tile has landed; was read by its products; an edge tile's load
+    // was issued (the check warps skip the other tiles, so they cannot follow
+    // `full` by its phases alone); an edge tile's values are in order
+    uint64_t full[10], empty[10], issued[10], fixed[10];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2];
+    Item item[2];
+    volatile int odd[2];                 // item count + 1 where an edge tile held inf or NaN
+    uint32_t tmem;
+    volatile int abort;
+};
+static_assert(sizeof(Bars) <= 1024, "barrier block");
+
+// Ring position: slot and phase parity.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step(int slots) {
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// Calls k(stream, j) and v(stream, j) for the key and value tiles of an item
+// in the order they go through the ring (stream 0 stands for both where the
+// keys are shared); false as soon as one of them fails.
+template <typename FK, typename FV>
+__device__ __forceinline__ bool for_tiles(const Item &w, FK k, FV v) {
+    if (shared_keys(w)) {
+        const int n = max(w.n0, w.n1);
+        if (n > 0 && !k(0, 0)) return false;
+        for (int j = 0; j < n; ++j) {
+            if (!v(0, j)) return false;
+            if (j + 1 < n && !k(0, j + 1)) return false;
+        }
+        return true;
+    }
+    if (!k(0, 0) || !k(1, 0)) return false;              // both streams have a tile
+    for (int j = 0; j < w.n0; ++j)                        // n0 >= n1
+        for (int s = 0; s < 2; ++s) {
+            const int n = stream_n(w, s);
+            if (j < n && !v(s, j)) return false;
+            if (j + 1 < n && !k(s, j + 1)) return false;
+        }
+    return true;
+}
+
+// ---------------------------------------------------------------- loads
+
+template <int D, bool kPaged>
+__device__ void load_role(const TcArgs &a, Bars *bar, uint8_t *sQ, uint8_t *sKV,
+                          const CUtensorMap *tm_q, const CUtensorMap *tm_k,
+                          const CUtensorMap *tm_v) {
+    constexpr int kAtoms = D / 64, kSlots = ring_slots<D>();
+    constexpr uint32_t kTile = 128 * D * 2;
+    const int lane = threadIdx.x % 32;
+    const int items = a.plan->items;
+    const uint32_t q_tile_bytes = (uint32_t)(a.c.half_tokens * a.s.R) * 128 * kAtoms;
+    Ring ring;
+    int b = 0, q_uses = 0;
+    bool ok = true;
+    for (int k = 0;; ++k) {
+        int item = blockIdx.x;
+        if (k > 0) {
+            if (lane == 0) item = gridDim.x + atomicAdd(a.next, 1);
+            item = __shfl_sync(0xffffffffu, item, 0);
+        }
+        const int slot = k & 1;
+        Item w{};
+        if (item < items) {
+            b = full_find_seq(a.seqs, a.s.B, b, item, lane);
+            w = make_item(a, a.seqs[b], b, item);
+        }
+        if (!tc::mbar_wait(&bar->item_empty[slot], ((k >> 1) & 1) ^ 1, a.err, &bar->abort)) break;
+        if (lane == 0) {
+            bar->item[slot] = w;
+            tc::mbar_arrive(&bar->item_full[slot]);
+        }
+        if (!w.valid) break;
+        if (w.n0 + w.n1 > 0) {
+            if (!tc::mbar_wait(&bar->q_empty, (q_uses & 1) ^ 1, a.err, &bar->abort)) break;
+            ++q_uses;
+            const int tiles = w.pair ? 2 : 1;
+            if (lane == 0) tc::mbar_expect_tx(&bar->q_full, q_tile_bytes * tiles);
+            __syncwarp();
+            if (lane < tiles * kAtoms) {
+                const int t = lane / kAtoms, at = lane % kAtoms;
+                tc::tma_load_3d(sQ + t * kTile + at * 16384, tm_q, &bar->q_full, at * 64,
+                                w.g * a.s.R, w.q0 + t * a.c.half_tokens);
+            }
+        }
+        const int limit = w.pos0 + w.nt;                 // no row attends key `limit` or later
+        int row[2] = {0, 0};                             // paged: this lane's box of the tile
+        auto load = [&](const CUtensorMap *tm, int s, int j, bool is_key) {
+            if (!tc::mbar_wait(&bar->empty[ring.slot], ring.phase ^ 1, a.err, &bar->abort))
+                return false;
+            uint8_t *dst = sKV + ring.slot * kTile;
+            uint64_t *full = &bar->full[ring.slot];
+            const int key = (stream_a(w, s) + j) * kFullKeys;
+            if (!kPaged) {
+                if (lane == 0) tc::mbar_expect_tx(full, kTile);
+                __syncwarp();
+                if (lane < kAtoms)
+                    tc::tma_load_3d(dst + lane * 16384, tm, full, lane * 64, w.g, w.k0 + key);
+            } else {
+                const int first = key + lane * a.box;    // this lane's box
+                const bool mine = lane * a.box < kFullKeys && first < limit;
+                if (is_key && mine) {
+                    const int pg = __ldg(a.q.block_table + (int64_t)w.b * a.s.max_pages +
+                                         first / a.s.page_size);
+                    const int rw = pg * a.s.page_size + first % a.s.page_size;
+                    if (s) row[1] = rw; else row[0] = rw;
+                }
+                const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+                if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)boxes * a.box * 128 * kAtoms);
+                __syncwarp();
+                if (mine) {
+                    const int rw = s ? row[1] : row[0];
+#pragma unroll
+                    for (int at = 0; at < kAtoms; ++at)
+                        tc::tma_load_3d(dst + at * 16384 + lane * a.box * 128, tm, full, at * 64,
+                                        w.g, rw);
+                }
+            }
+            if (!is_key && lane == 0 && edge_tile(w, stream_a(w, s) + j))
+                tc::mbar_arrive(&bar->issued[ring.slot]);
+            ring.step(kSlots);
+            return true;
+        };
+        ok = for_tiles(w, [&](int s, int j) { return load(tm_k, s, j, true); },
+                       [&](int s, int j) { return load(tm_v, s, j, false); });
+        if (!ok) break;
+    }
+    if (bar->abort) {
+        // copies in flight land before the CTA may end (each slot's latest
+        // load), with a limit
+        for (int i = 0; i < kSlots; ++i) {
+            const bool this_lap = i < ring.slot;
+            if (!this_lap && ring.phase == 0) continue;  // never loaded
+            const uint32_t parity = this_lap ? ring.phase : ring.phase ^ 1;
+            for (int n = 0; n < 1000 && !tc::mbar_try_wait(&bar->full[i], parity); ++n) {}
+        }
+        for (int n = 0; q_uses > 0 && n < 1000 &&
+                        !tc::mbar_try_wait(&bar->q_full, (q_uses - 1) & 1); ++n) {}
+    }
+}
+
+// ---------------------------------------------------------------- MMA
+
+template <int D>
+__device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ, uint32_t sKV) {
+    constexpr int kSlots = ring_slots<D>();
+    constexpr uint32_t kTile = 128 * D * 2;
+    constexpr uint32_t idesc_s = tc::idesc_bf16(kRows, kFullKeys, 0, 0);
+    constexpr uint32_t idesc_o = tc::idesc_bf16(kRows, D, 0, 1);
+    Ring ring;
+    uint32_t fix_phase = 0;                              // per slot
+    uint32_t p_phase = 0;                                // per stream
+    int q_uses = 0;
+    for (int k = 0;; ++k) {
+        const int slot = k & 1;
+        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort)) return;
+        const Item w = bar->item[slot];
+        tc::mbar_arrive(&bar->item_empty[slot]);
+        if (!w.valid) return;
+        const int total = w.n0 + w.n1;
+        if (total == 0) continue;
+        if (!tc::mbar_wait(&bar->q_full, q_uses & 1, a.err, &bar->abort)) return;
+        ++q_uses;
+        int issued = 0;
+        // S of stream s from the key tile in slot ks
+        auto scores = [&](int s, int ks) {
+            const uint32_t qa = sQ + (w.pair && s ? kTile : 0), ka = sKV + ks * kTile;
+            tc::tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const uint64_t ad = tc::sdesc_sw128(qa + (i / 4) * 16384 + (i % 4) * 32, 16, 1024);
+                const uint64_t bd = tc::sdesc_sw128(ka + (i / 4) * 16384 + (i % 4) * 32, 16, 1024);
+                tc::mma_ss(tmem + s * 128, ad, bd, idesc_s, i > 0);
+            }
+            tc::mma_commit(&bar->s_full[s]);
+            if (++issued == total) tc::mma_commit(&bar->q_empty);
+        };
+        // O of stream s from the value tile in slot vs
+        auto values = [&](int s, int j, int vs) {
+            if (!tc::mbar_wait(&bar->p_full[s], (p_phase >> s) & 1, a.err, &bar->abort))
+                return false;
+            p_phase ^= 1u << s;
+            tc::tc_fence_after();
+            const uint32_t va = sKV + vs * kTile;
+#pragma unroll
+            for (int i = 0; i < kFullKeys / 16; ++i) {
+                const uint64_t bd = tc::sdesc_sw128(va + i * 2048, 16384, 1024);
+                tc::mma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, bd, idesc_o,
+                           (j > 0 || i > 0) ? 1u : 0u);
+            }
+            if (j + 1 == stream_n(w, s)) tc::mma_commit(&bar->o_full[s]);
+            return true;
+        };
+        auto take = [&](int *at) {                       // the ring's next tile has landed
+            *at = ring.slot;
+            const bool ok = tc::mbar_wait(&bar->full[ring.slot], ring.phase, a.err, &bar->abort);
+            ring.step(kSlots);
+            return ok;
+        };
+        auto checked = [&](int s, int j, int vs) {       // an edge tile's values are in order
+            if (!edge_tile(w, stream_a(w, s) + j)) return true;
+            const bool ok = tc::mbar_wait(&bar->fixed[vs], (fix_phase >> vs) & 1, a.err, &bar->abort);
+            fix_phase ^= 1u << vs;
+            return ok;
+        };
+        int ks = 0, vs = 0;
+        if (shared_keys(w)) {
+            const int n = max(w.n0, w.n1);
+            if (!take(&ks)) return;
+            if (w.n0 > 0) scores(0, ks);
+            if (w.n1 > 0) scores(1, ks);
+            tc::mma_commit(&bar->empty[ks]);
+            for (int j = 0; j < n; ++j) {
+                if (!take(&vs) || !checked(0, j, vs)) return;
+                bool have = false;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (j < stream_n(w, s) && !values(s, j, vs)) return;
+                    if (j + 1 < n && !have) {
+                        if (!take(&ks)) return;
+                        have = true;
+                    }
+                    if (j + 1 < stream_n(w, s)) scores(s, ks);
+                }
+                tc::mma_commit(&bar->empty[vs]);
+                if (have) tc::mma_commit(&bar->empty[ks]);
+            }
+        } else {
+            for (int s = 0; s < 2; ++s) {
+                if (!take(&ks)) return;
+                scores(s, ks);
+                tc::mma_commit(&bar->empty[ks]);
+            }
+            for (int j = 0; j < w.n0; ++j)
+                for (int s = 0; s < 2; ++s) {
+                    const int n = stream_n(w, s);
+                    if (j >= n) continue;
+                    if (!take(&vs) || !checked(s, j, vs) || !values(s, j, vs)) return;
+                    tc::mma_commit(&bar->empty[vs]);
+                    if (j + 1 < n) {
+                        if (!take(&ks)) return;
+                        scores(s, ks);
+                        tc::mma_commit(&bar->empty[ks]);
+                    }
+                }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- value check
+
+// Two warps.  In a tile that some row attends only in part, P is 0 at the
+// keys the row does not attend, and 0 times infinity or NaN would reach it:
+// rows of V that no row attends (other sequences, what a page held before)
+// are set to 0, and in rows that only later tokens attend, infinities and
+// NaN are (the epilogue adds them for the rows that do attend them).
+template <int D>
+__device__ void check_role(const TcArgs &a, Bars *bar, uint8_t *sKV) {
+    constexpr int kSlots = ring_slots<D>(), kChunks = D / 8;
+    const int lane = threadIdx.x % 32, half = (threadIdx.x / 32) & 1;
+    Ring ring;
+    uint32_t edge_phase = 0;                             // per slot
+    for (int k = 0;; ++k) {
+        const int slot = k & 1;
+        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort)) return;
+        const Item w = bar->item[slot];
+        if (w.valid) {
+            const int limit = w.pos0 + w.nt;
+            auto key = [&](int, int) {
+                ring.step(kSlots);
+                return true;
+            };
+            auto value = [&](int s, int j) {
+                const int t = stream_a(w, s) + j;
+                if (edge_tile(w, t)) {
+                    if (!tc::mbar_wait(&bar->issued[ring.slot], (edge_phase >> ring.slot) & 1,
+                                       a.err, &bar->abort))
+                        return false;
+                    edge_phase ^= 1u << ring.slot;
+                    if (!tc::mbar_wait(&bar->full[ring.slot], ring.phase, a.err, &bar->abort))
+                        return false;
+                    uint8_t *base = sKV + ring.slot * (128 * D * 2);
+                    const int from = max(0, w.pos0 + 1 - t * kFullKeys);
+                    bool odd = false;
+                    for (int i = half * 32 + lane; i < (kFullKeys - from) * kChunks; i += 64) {
+                        const int r = from + i / kChunks, ch = i % kChunks;
+                        uint4 *p = (uint4 *)(base + (ch / 8) * 16384 + r * 128 +
+                                             (((ch % 8) ^ (r & 7)) << 4));
+                        if (t * kFullKeys + r >= limit) {
+                            *p = make_uint4(0u, 0u, 0u, 0u);
+                            continue;
+                        }
+                        uint4 v = *p;
+                        uint32_t *x = (uint32_t *)&v;
+                        bool hit = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if ((x[e] & 0x7f80u) == 0x7f80u) { x[e] &= 0xffff0000u; hit = true; }
+                            if ((x[e] & 0x7f800000u) == 0x7f800000u) { x[e] &= 0xffffu; hit = true; }
+                        }
+                        if (hit) {
+                            *p = v;
+                            odd = true;
+                        }
+                    }
+                    if (odd) bar->odd[slot] = k + 1;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __threadfence_block();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar->fixed[ring.slot]);
+                }
+                ring.step(kSlots);
+                return true;
+            };
+            if (!for_tiles(w, key, value)) return;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar->item_empty[slot]);
+        if (!w.valid) return;
+    }
+}
+
+// ---------------------------------------------------------------- softmax
+
+template <int D, bool kPaged>
+__device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
+    const int quad = (threadIdx.x / 32) % 4, lane = threadIdx.x % 32;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + s * 128 + lane_off, tO = tmem + 256 + s * 128 + lane_off;
+    const int row = quad * 32 + lane;
+    const int tok = row / a.s.R, head = row % a.s.R;
+    uint32_t s_phase = 0, o_phase = 0;
+    for (int k = 0;; ++k) {
+        const int slot = k & 1;
+        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort)) return;
+        const Item w = bar->item[slot];
+        if (!w.valid) return;
+        const int first_tok = w.pair ? s * a.c.half_tokens : 0;
+        const int toks = min(a.c.half_tokens, w.nt - first_tok);
+        const bool valid = tok < toks;
+        const bool busy = quad * 32 < toks * a.s.R;      // the warp holds a row
+        const int pos = w.pos0 + first_tok + tok;
+        const int t0 = stream_a(w, s), n = stream_n(w, s);
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < n; ++j) {
+            if (!tc::mbar_wait(&bar->s_full[s], s_phase, a.err, &bar->abort)) return;
+            s_phase ^= 1;
+            if (busy) {
+                tc::tc_fence_after();
+                uint32_t v[128];
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) tc::tmem_ld32(tS + c, *(uint32_t(*)[32])(v + c));
+                tc::tmem_ld_wait();
+                const int key0 = (t0 + j) * kFullKeys;
+                if (key0 + kFullKeys > w.pos0 + first_tok + 1) {
+                    const int lim = pos - key0;          // columns above lim are not attended
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c > lim) v[c] = __float_as_uint(-INFINITY);
+                }
+                float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
+#pragma unroll
+                for (int c = 0; c < 128; c += 8) {
+                    m0 = tc::fmax3(m0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                    m1 = tc::fmax3(m1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+                    m2 = tc::fmax3(m2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
+                    m3 = tc::fmax3(m3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
+                }
+                const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                // S(j) is complete, and with it (one thread issues both, in
+                // order) the product P V of tile j - 1: O may be rescaled
+                const bool move = (top - m) * a.scale_log2 > kMaxLag;
+                if (j == 0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, move)) {
+                    const float f = move ? tc::ex2_approx((m - top) * a.scale_log2) : 1.f;
+                    if (move) m = top;
+                    l *= f;
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(tO + c, o);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tc::tmem_st32(tO + c, o);
+                    }
+                }
+                const float mb = m == -INFINITY ? 0.f : m * a.scale_log2;
+                float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+                for (int h = 0; h < 128; h += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        const float e0 = tc::ex2_approx(fmaf(__uint_as_float(v[h + c]), a.scale_log2, -mb));
+                        const float e1 = tc::ex2_approx(fmaf(__uint_as_float(v[h + c + 1]), a.scale_log2, -mb));
+                        const float e2 = tc::ex2_approx(fmaf(__uint_as_float(v[h + c + 2]), a.scale_log2, -mb));
+                        const float e3 = tc::ex2_approx(fmaf(__uint_as_float(v[h + c + 3]), a.scale_log2, -mb));
+                        l0 += e0; l1 += e1; l2 += e2; l3 += e3;
+                        __nv_bfloat162 b0 = __floats2bfloat162_rn(e0, e1);
+                        __nv_bfloat162 b1 = __floats2bfloat162_rn(e2, e3);
+                        pk[c / 2] = *(uint32_t *)&b0;
+                        pk[c / 2 + 1] = *(uint32_t *)&b1;
+                    }
+                    tc::tmem_st16(tS + h / 2, pk);
+                }
+                l += (l0 + l1) + (l2 + l3);
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar->p_full[s]);
+        }
+        // epilogue: O / l and the log-sum-exp, final or as one of the row's parts
+        if (n > 0) {
+            if (!tc::mbar_wait(&bar->o_full[s], o_phase, a.err, &bar->abort)) return;
+            o_phase ^= 1;
+            tc::tc_fence_after();
+        }
+        if (busy && (w.pair || s == 0 || a.c.max_parts > 1)) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float out_lse = l == 0.f ? -INFINITY : m * a.s.scale + logf(l);
+            const int64_t at = (int64_t)(w.q0 + first_tok + tok) * a.s.Hq + w.g * a.s.R + head;
+            const int64_t part = ((int64_t)w.part + (w.pair ? 0 : s)) * a.s.tokens * a.s.Hq + at;
+            const bool odd = bar->odd[slot] == k + 1;
+            const bool some = __any_sync(0xffffffffu, valid && l != 0.f);
+            if (valid) {
+                if (w.parts > 0) a.part_lse[part] = out_lse;
+                else a.lse[at] = out_lse;
+            }
+            if (some || w.parts == 0) {
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    if (n > 0) {
+                        tc::tmem_ld32(tO + c, o);
+                        tc::tmem_ld_wait();
+                    }
+                    float x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
+                    if (odd && valid) {
+                        const int hi = min(pos, (t0 + n) * kFullKeys - 1);
+                        for (int jk = max(t0 * kFullKeys, w.pos0 + 1); jk <= hi; ++jk) {
+                            int64_t kr = (int64_t)w.k0 + jk;
+                            if (kPaged)
+                                kr = (int64_t)a.q.block_table[(int64_t)w.b * a.s.max_pages +
+                                                              jk / a.s.page_size] * a.s.page_size +
+                                     jk % a.s.page_size;
+                            const __nv_bfloat16 *vp = a.V + kr * a.s.v_stride + (int64_t)w.g * D + c;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float f = __bfloat162float(vp[i]);
+                                if (!isfinite(f)) x[i] += f;
+                            }
+                        }
+                    }
+                    if (valid && w.parts > 0) {
+                        float4 *dst = (float4 *)(a.part_o + part * D + c);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            dst[i / 4] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                    } else if (valid) {
+                        uint4 *dst = (uint4 *)(a.O + at * D + c);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            uint4 u;
+                            __nv_bfloat162 *h = (__nv_bfloat162 *)&u;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                h[e] = __floats2bfloat162_rn(x[i + 2 * e], x[i + 2 * e + 1]);
+                            dst[i / 8] = u;
+                        }
+                    }
+                }
+            }
+            tc::tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar->item_empty[slot]);
+    }
+}
+
+template <int D, bool kPaged>
+__global__ void __launch_bounds__(kThreads, 1)
+full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcArgs a) {
+    constexpr int kSlots = ring_slots<D>();
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sQ = smem;                                  // [2][D / 64][128][64]
+    uint8_t *sKV = sQ + 2 * 128 * D * 2;                 // [kSlots][D / 64][128][64]
+    Bars *bar = (Bars *)(sKV + kSlots * 128 * D * 2);
+    const int warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            tc::mbar_init(&bar->full[i], 1);
+            tc::mbar_init(&bar->empty[i], 1);
+            tc::mbar_init(&bar->issued[i], 1);
+            tc::mbar_init(&bar->fixed[i], 2);
+        }
+        tc::mbar_init(&bar->q_full, 1);
+        tc::mbar_init(&bar->q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bar->s_full[i], 1);
+            tc::mbar_init(&bar->p_full[i], 4);           // one per softmax warp
+            tc::mbar_init(&bar->o_full[i], 1);
+            tc::mbar_init(&bar->item_full[i], 1);
+            tc::mbar_init(&bar->item_empty[i], 1 + 2 + 8);   // MMA, check and softmax warps
+            bar->odd[i] = 0;
+        }
+        bar->abort = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 1) tc::tmem_alloc(&bar->tmem, 512);
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = bar->tmem;
+    if (warp < 4) {
+        tc::regs_dec<kRegsLoad>();
+        if (warp == 0) load_role<D, kPaged>(a, bar, sQ, sKV, &tm_q, &tm_k, &tm_v);
+        else if (warp == 1) {
+            if (threadIdx.x % 32 == 0)
+                mma_role<D>(a, bar, tmem, tc::smem_u32(sQ), tc::smem_u32(sKV));
+        } else check_role<D>(a, bar, sKV);
+    } else {
+        tc::regs_inc<kRegsSoftmax>();
+        softmax_role<D, kPaged>(a, bar, tmem, warp / 4 - 1);
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_free(tmem, 512);
+    }
+}
+
+int sm_count() {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+template <int D, bool kPaged>
+cudaError_t launch_tc_t(const FullShape &s, const TcArgs &a, const void *Q, const void *K,
+                        const void *V, cudaStream_t st) {
+    CUtensorMap tq, tk, tv;
+    const uint64_t qdims[3] = {(uint64_t)D, (uint64_t)s.Hq, (uint64_t)s.tokens};
+    const uint64_t qstr[2] = {(uint64_t)D * 2, (uint64_t)s.q_stride * 2};
+    const uint32_t qbox[3] = {64, (uint32_t)s.R, (uint32_t)a.c.half_tokens};
+    if (!make_tmap_bf16(&tq, Q, 3, qdims, qstr, qbox)) return cudaErrorInvalidValue;
+    // no keys at all: nothing is loaded, but a map needs an extent
+    const uint64_t rows = (uint64_t)std::max<int64_t>(s.key_tokens, 1);
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)s.Hkv, rows};
+    const uint64_t kstr[2] = {(uint64_t)D * 2, (uint64_t)s.k_stride * 2};
+    const uint64_t vstr[2] = {(uint64_t)D * 2, (uint64_t)s.v_stride * 2};
+    const uint32_t box[3] = {64, 1, (uint32_t)a.box};
+    if (!make_tmap_bf16(&tk, s.key_tokens ? K : Q, 3, dims, kstr, box)) return cudaErrorInvalidValue;
+    if (!make_tmap_bf16(&tv, s.key_tokens ? V : Q, 3, dims, vstr, box)) return cudaErrorInvalidValue;
+    auto k = full_tc_kernel<D, kPaged>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)tc_smem<D>());
+    if (e != cudaSuccess) return e;
+    const int64_t most = (s.tokens / a.c.unit_tokens + std::min<int64_t>(s.B, s.tokens)) * s.Hkv *
+                         a.c.max_parts;
+    k<<<(unsigned)std::min<int64_t>(most, sm_count()), kThreads, tc_smem<D>(), st>>>(tq, tk, tv, a);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Two row tiles of 128 / R tokens a unit.  Keys are split into runs while a
+// call has too few units to keep every SM busy several times over: about
+// kItemsPerSm items an SM, runs of at least kMinTiles tiles; the partial
+// results then take at most (items + units) * 256 rows * 2 (about 300 MB).
+FullCut full_tc_cut(const FullShape &s) {
+    constexpr int kItemsPerSm = 6, kMinTiles = 2, kSms = 148;
+    FullCut c;
+    c.half_tokens = kRows / s.R;
+    c.unit_tokens = 2 * c.half_tokens;
+    c.split = kSms * kItemsPerSm;
+    c.min_tiles = kMinTiles;
+    const int64_t units = std::max<int64_t>(1, (s.tokens + c.unit_tokens - 1) / c.unit_tokens) * s.Hkv;
+    c.max_parts = (int)std::min<int64_t>(64, std::max<int64_t>(1, (4 * kSms + units - 1) / units));
+    return c;
+}
+
+cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut &c,
+                           const FullPlan *plan, const FullSeq *seqs, const void *Q,
+                           const void *K, const void *V, void *O, float *lse, float *part_o,
+                           float *part_lse, uint32_t *err, cudaStream_t st) {
+    TcArgs a;
+    a.s = s; a.q = q; a.c = c;
+    a.plan = plan; a.seqs = seqs;
+    a.next = (int *)&plan->next;
+    a.V = (const __nv_bfloat16 *)V;
+    a.O = (__nv_bfloat16 *)O;
+    a.lse = lse; a.part_o = part_o; a.part_lse = part_lse; a.err = err;
+    a.scale_log2 = s.scale * kLog2e;
+    a.box = kFullKeys;                   // the largest power of two that divides pages and tiles
+    if (s.paged)
+        while (s.page_size % a.box != 0) a.box /= 2;
+    if (s.d == 64)
+        return s.paged ? launch_tc_t<64, true>(s, a, Q, K, V, st)
+                       : launch_tc_t<64, false>(s, a, Q, K, V, st);
+    return s.paged ? launch_tc_t<128, true>(s, a, Q, K, V, st)
+                   : launch_tc_t<128, false>(s, a, Q, K, V, st);
+}
+
+}  // namespace msa

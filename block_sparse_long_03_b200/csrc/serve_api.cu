@@ -104,7 +104,9 @@ msa_status_t make_full(const msa_attn_params_t *p, bool paged, FullShape *s) {
     return MSA_OK;
 }
 
-FullCut full_cut(const FullShape &s) { return full_simt_cut(s); }
+FullCut full_cut(const FullShape &s) {
+    return s.dtype == MSA_BF16 ? full_tc_cut(s) : full_simt_cut(s);
+}
 
 // Workspace: [error word][plan][sequences][partial O][partial lse]
 struct FullLayout {
@@ -153,7 +155,15 @@ msa_status_t run_full(const msa_attn_params_t *params, bool paged, const void *Q
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = launch_full_plan(s, q, c, plan, seqs, err, st);
     if (s.tokens == 0) return cuda_status(e);
-    if (e == cudaSuccess) e = launch_full_simt(s, q, c, plan, seqs, Q, K, V, O, lse, st);
+    if (s.dtype == MSA_F32) {
+        if (e == cudaSuccess) e = launch_full_simt(s, q, c, plan, seqs, Q, K, V, O, lse, st);
+        return cuda_status(e);
+    }
+    float *part_o = (float *)(ws + L.part_o), *part_lse = (float *)(ws + L.part_lse);
+    if (e == cudaSuccess)
+        e = launch_full_tc(s, q, c, plan, seqs, Q, K, V, O, lse, part_o, part_lse, err, st);
+    if (e == cudaSuccess && c.max_parts > 1)
+        e = launch_full_combine(s, q, c, plan, seqs, part_o, part_lse, O, lse, st);
     return cuda_status(e);
 }
 

@@ -287,9 +287,9 @@ def test_graphs_and_streams():
         torch.cuda.synchronize()
         with torch.cuda.graph(graph):
             msa.attn_paged(*args, out=out, lse=lse, workspace=ws)
-        cases.append((args, out, lse, graph))
+        cases.append((args, out, lse, graph, ws))      # a graph's workspace lives as long as it
     for k in range(3):
-        for args, out, lse, graph in cases:
+        for args, out, lse, graph, _ in cases:
             args[0].mul_(0.5)
             args[4].sub_(1).clamp_(min=31 if args[0].shape[0] == 32 else 1)
             graph.replay()
