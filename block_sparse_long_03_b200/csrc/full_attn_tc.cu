@@ -54,7 +54,7 @@ struct TcArgs {
     float *lse, *part_o, *part_lse;
     uint32_t *err;
     int box;                             // key rows of one TMA box
-    float scale_log2;
+    float scale_log2, lag;               // lag: kMaxLag in units of raw scores
 };
 
 // A work item as the loading warp hands it to the others.
@@ -444,6 +444,132 @@ __device__ void check_role(const TcArgs &a, Bars *bar, uint8_t *sKV) {
 
 // ---------------------------------------------------------------- softmax
 
+// Two fp32 values in one 64-bit register: the packed operations do two
+// additions or multiply-adds an issue slot.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// max(a, b, c), NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 2^x of two values x <= 2^7 on the multiply-add pipe.  With n = round(x) and
+// f = x - n in [-1/2, 1/2]: 2^x = 2^n p(f), p the polynomial of degree 4 with
+// the least largest relative error to 2^f there (found by iteratively
+// reweighted least squares): 2.7e-6, mean 4e-8.  n comes from adding
+// 1.5 * 2^23, whose sum's low bits are n; they are added to p's exponent.
+// x below -126 counts as -126.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
+    float x, y;
+    unpack2(x2, x, y);
+    x2 = pack2(fmaxf(x, -126.f), fmaxf(y, -126.f));
+    const float kRound = 12582912.f;
+    const uint64_t r2 = add2(x2, pack2(kRound, kRound));
+    const uint64_t n2 = add2(r2, pack2(-kRound, -kRound));
+    const uint64_t f2 = fma2(n2, pack2(-1.f, -1.f), x2);
+    uint64_t p2 = fma2(f2, pack2(0.009570101276040077f, 0.009570101276040077f),
+                       pack2(0.05591785907745361f, 0.05591785907745361f));
+    p2 = fma2(p2, f2, pack2(0.240247443318367f, 0.240247443318367f));
+    p2 = fma2(p2, f2, pack2(0.6931217908859253f, 0.6931217908859253f));
+    p2 = fma2(p2, f2, pack2(0.9999992847442627f, 0.9999992847442627f));
+    float r, q, p, u;
+    unpack2(r2, r, q);
+    unpack2(p2, p, u);
+    return pack2(__uint_as_float(__float_as_uint(p) + (__float_as_uint(r) << 23)),
+                 __uint_as_float(__float_as_uint(u) + (__float_as_uint(q) << 23)));
+}
+
+// The row's maximum over the attended columns of an S tile.
+template <bool kEdge>
+__device__ __forceinline__ float row_max(uint32_t tS, int lim) {
+    float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
+#pragma unroll 1
+    for (int h = 0; h < 128; h += 64) {
+        uint32_t v[64];
+        tc::tmem_ld32(tS + h, *(uint32_t(*)[32])v);
+        tc::tmem_ld32(tS + h + 32, *(uint32_t(*)[32])(v + 32));
+        tc::tmem_ld_wait();
+        if (kEdge) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+                if (h + c > lim) v[c] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += 8) {
+            m0 = max3_nan(m0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+            m1 = max3_nan(m1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+            m2 = max3_nan(m2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
+            m3 = max3_nan(m3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
+        }
+    }
+    return max3_nan(max3_nan(m0, m1, m2), m3, m3);
+}
+
+#ifndef POLY
+#define POLY 5
+#endif
+// P = 2^(scale_log2 S - mb) of an S tile, as bf16 over the columns already
+// read; returns the fp32 row sum.  Every 32 columns, kPoly of the 16 pairs go
+// to the multiply-add pipe and the others to the special-function unit, which
+// alone would bound the kernel.
+template <bool kEdge>
+__device__ __forceinline__ float weights(uint32_t tS, int lim, float scale_log2, float mb) {
+    constexpr int kPoly = kEdge ? 0 : POLY;
+    const uint64_t scale2 = pack2(scale_log2, scale_log2), mb2 = pack2(-mb, -mb);
+    uint64_t l0 = 0, l1 = 0;                             // (0, 0)
+#pragma unroll 1
+    for (int h = 0; h < 128; h += 32) {
+        uint32_t v[32], pk[16];
+        tc::tmem_ld32(tS + h, v);
+        tc::tmem_ld_wait();
+        if (kEdge) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                if (h + c > lim) v[c] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            uint64_t x2 = fma2(pack2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])),
+                               scale2, mb2);
+            float e0, e1;
+            if ((c + 1) * kPoly / 16 > c * kPoly / 16) {
+                x2 = exp2_poly2(x2);
+                unpack2(x2, e0, e1);
+            } else {
+                unpack2(x2, e0, e1);
+                e0 = tc::ex2_approx(e0);
+                e1 = tc::ex2_approx(e1);
+                x2 = pack2(e0, e1);
+            }
+            if (c & 1) l1 = add2(l1, x2); else l0 = add2(l0, x2);
+            __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
+            pk[c] = *(uint32_t *)&b;
+        }
+        tc::tmem_st16(tS + h / 2, pk);
+    }
+    float a, b;
+    unpack2(add2(l0, l1), a, b);
+    return a + b;
+}
+
 template <int D, bool kPaged>
 __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
     const int quad = (threadIdx.x / 32) % 4, lane = threadIdx.x % 32;
@@ -469,36 +595,22 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
             s_phase ^= 1;
             if (busy) {
                 tc::tc_fence_after();
-                uint32_t v[128];
-#pragma unroll
-                for (int c = 0; c < 128; c += 32) tc::tmem_ld32(tS + c, *(uint32_t(*)[32])(v + c));
-                tc::tmem_ld_wait();
                 const int key0 = (t0 + j) * kFullKeys;
-                if (key0 + kFullKeys > w.pos0 + first_tok + 1) {
-                    const int lim = pos - key0;          // columns above lim are not attended
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c > lim) v[c] = __float_as_uint(-INFINITY);
-                }
-                float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
-#pragma unroll
-                for (int c = 0; c < 128; c += 8) {
-                    m0 = tc::fmax3(m0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-                    m1 = tc::fmax3(m1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
-                    m2 = tc::fmax3(m2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
-                    m3 = tc::fmax3(m3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
-                }
-                const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                // columns above lim are not attended by this row
+                const bool edge = key0 + kFullKeys > w.pos0 + first_tok + 1;
+                const int lim = edge ? pos - key0 : kFullKeys;
+                float top = edge ? row_max<true>(tS, lim) : row_max<false>(tS, lim);
                 // S(j) is complete, and with it (one thread issues both, in
-                // order) the product P V of tile j - 1: O may be rescaled
-                const bool move = (top - m) * a.scale_log2 > kMaxLag;
+                // order) the product P V of tile j - 1: O may be rescaled.
+                // Not "top > m + lag", so that a NaN moves m too.
+                const bool move = !(top <= m + a.lag);
                 if (j == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, move)) {
                     const float f = move ? tc::ex2_approx((m - top) * a.scale_log2) : 1.f;
                     if (move) m = top;
                     l *= f;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
                         tc::tmem_ld32(tO + c, o);
@@ -510,25 +622,9 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                     }
                 }
                 const float mb = m == -INFINITY ? 0.f : m * a.scale_log2;
-                float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-                for (int h = 0; h < 128; h += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float e0 = tc::ex2_approx(fmaf(__uint_as_float(v[h + c]), a.scale_log2, -mb));
-                        const float e1 = tc::ex2_approx(fmaf(__uint_as_float(v[h + c + 1]), a.scale_log2, -mb));
-                        const float e2 = tc::ex2_approx(fmaf(__uint_as_float(v[h + c + 2]), a.scale_log2, -mb));
-                        const float e3 = tc::ex2_approx(fmaf(__uint_as_float(v[h + c + 3]), a.scale_log2, -mb));
-                        l0 += e0; l1 += e1; l2 += e2; l3 += e3;
-                        __nv_bfloat162 b0 = __floats2bfloat162_rn(e0, e1);
-                        __nv_bfloat162 b1 = __floats2bfloat162_rn(e2, e3);
-                        pk[c / 2] = *(uint32_t *)&b0;
-                        pk[c / 2 + 1] = *(uint32_t *)&b1;
-                    }
-                    tc::tmem_st16(tS + h / 2, pk);
-                }
-                l += (l0 + l1) + (l2 + l3);
+                const float sum = edge ? weights<true>(tS, lim, a.scale_log2, mb)
+                                       : weights<false>(tS, lim, a.scale_log2, mb);
+                if (m != -INFINITY) l += sum;            // (a row of -inf scores has no weight)
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
             }
@@ -553,7 +649,7 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                 else a.lse[at] = out_lse;
             }
             if (some || w.parts == 0) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     __syncwarp();
@@ -726,6 +822,7 @@ cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut 
     a.O = (__nv_bfloat16 *)O;
     a.lse = lse; a.part_o = part_o; a.part_lse = part_lse; a.err = err;
     a.scale_log2 = s.scale * kLog2e;
+    a.lag = kMaxLag / a.scale_log2;
     a.box = kFullKeys;                   // the largest power of two that divides pages and tiles
     if (s.paged)
         while (s.page_size % a.box != 0) a.box /= 2;
