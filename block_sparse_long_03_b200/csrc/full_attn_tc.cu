@@ -54,6 +54,7 @@ struct TcArgs {
     float *lse, *part_o, *part_lse;
     uint32_t *err;
     int box;                             // key rows of one TMA box
+    bool wide;                           // O is 32-byte aligned
     float scale_log2, lag;               // lag: kMaxLag in units of raw scores
 };
 
@@ -117,13 +118,24 @@ struct Bars {
     // was issued (the check warps skip the other tiles, so they cannot follow
     // `full` by its phases alone); an edge tile's values are in order
     uint64_t full[10], empty[10], issued[10], fixed[10];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2];
+    uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], turn[2][4], item_full[2], item_empty[2];
     Item item[2];
     volatile int odd[2];                 // item count + 1 where an edge tile held inf or NaN
     uint32_t tmem;
     volatile int abort;
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
+
+// One lane's arrival, without a branch and without the release fence of a
+// plain arrival (together about 150 cycles of a softmax tile).  What it
+// announces is in TMEM, ordered by tcgen05.wait::st and the fences around it,
+// or nothing but the turn itself.
+__device__ __forceinline__ void arrive_if(bool pred, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];\n\t}\n"
+        ::"r"(tc::smem_u32(bar)), "r"((uint32_t)pred) : "memory");
+}
 
 // Ring position: slot and phase parity.
 struct Ring {
@@ -263,15 +275,36 @@ __device__ void load_role(const TcArgs &a, Bars *bar, uint8_t *sQ, uint8_t *sKV,
 
 // ---------------------------------------------------------------- MMA
 
+// A shared-memory matrix descriptor (128-byte swizzle, 8-row groups 1024 bytes
+// apart) from its low word: the address / 16, with the leading byte offset
+// / 16 in the upper half.  Kept in this form because one thread issues all
+// products, and an address step is then one addition: 16 products in 1032
+// cycles where building each descriptor from its address took 1097 (ideal
+// 1024).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+    return (saddr >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc(uint32_t lo) {
+    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);   // group stride, version, swizzle
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+
+// One thread issues the products of one stream.  The two streams' threads sit
+// in different warps and do not wait for each other: with one thread for both,
+// its waits and commits (about 900 cycles a tile) were the kernel's bound.
 template <int D>
-__device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ, uint32_t sKV) {
+__device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ, uint32_t sKV,
+                         int me) {
     constexpr int kSlots = ring_slots<D>();
     constexpr uint32_t kTile = 128 * D * 2;
     constexpr uint32_t idesc_s = tc::idesc_bf16(kRows, kFullKeys, 0, 0);
     constexpr uint32_t idesc_o = tc::idesc_bf16(kRows, D, 0, 1);
+    const uint32_t tS = tmem + me * 128, tO = tmem + 256 + me * 128;
     Ring ring;
     uint32_t fix_phase = 0;                              // per slot
-    uint32_t p_phase = 0;                                // per stream
+    uint32_t p_phase = 0;
     int q_uses = 0;
     for (int k = 0;; ++k) {
         const int slot = k & 1;
@@ -279,99 +312,87 @@ __device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ,
         const Item w = bar->item[slot];
         tc::mbar_arrive(&bar->item_empty[slot]);
         if (!w.valid) return;
-        const int total = w.n0 + w.n1;
-        if (total == 0) continue;
+        if (w.n0 + w.n1 == 0) continue;
         if (!tc::mbar_wait(&bar->q_full, q_uses & 1, a.err, &bar->abort)) return;
         ++q_uses;
-        int issued = 0;
-        // S of stream s from the key tile in slot ks
-        auto scores = [&](int s, int ks) {
-            const uint32_t qa = sQ + (w.pair && s ? kTile : 0), ka = sKV + ks * kTile;
+        const bool shared = shared_keys(w);
+        const int n = stream_n(w, me);
+        if (n == 0) tc::mbar_arrive(&bar->q_empty);
+        const uint32_t qa = desc_lo(sQ + (w.pair && me ? kTile : 0), 16);
+        // Both threads wait for every tile and release every tile, so that
+        // neither can be a lap of the ring ahead of the other (a phase's
+        // parity tells one lap only).
+        int held = -1;                                   // a value slot not yet released
+        bool seen = false;                               // the next key tile was waited for
+        auto key = [&](int s, int j) {
+            const int at = ring.slot;
+            const uint32_t phase = ring.phase;
+            ring.step(kSlots);
+            if (!seen && !tc::mbar_wait(&bar->full[at], phase, a.err, &bar->abort)) return false;
+            seen = false;
+            if (shared ? j >= n : s != me) {
+                tc::mbar_arrive(&bar->empty[at]);
+                return true;
+            }
+            const uint32_t ka = desc_lo(sKV + at * kTile, 16);
             tc::tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const uint64_t ad = tc::sdesc_sw128(qa + (i / 4) * 16384 + (i % 4) * 32, 16, 1024);
-                const uint64_t bd = tc::sdesc_sw128(ka + (i / 4) * 16384 + (i % 4) * 32, 16, 1024);
-                tc::mma_ss(tmem + s * 128, ad, bd, idesc_s, i > 0);
-            }
-            tc::mma_commit(&bar->s_full[s]);
-            if (++issued == total) tc::mma_commit(&bar->q_empty);
-        };
-        // O of stream s from the value tile in slot vs
-        auto values = [&](int s, int j, int vs) {
-            if (!tc::mbar_wait(&bar->p_full[s], (p_phase >> s) & 1, a.err, &bar->abort))
-                return false;
-            p_phase ^= 1u << s;
-            tc::tc_fence_after();
-            const uint32_t va = sKV + vs * kTile;
-#pragma unroll
-            for (int i = 0; i < kFullKeys / 16; ++i) {
-                const uint64_t bd = tc::sdesc_sw128(va + i * 2048, 16384, 1024);
-                tc::mma_ts(tmem + 256 + s * 128, tmem + s * 128 + i * 8, bd, idesc_o,
-                           (j > 0 || i > 0) ? 1u : 0u);
-            }
-            if (j + 1 == stream_n(w, s)) tc::mma_commit(&bar->o_full[s]);
+            for (int i = 0; i < D / 16; ++i)
+                tc::mma_ss(tS, desc(qa + (i / 4) * 1024 + (i % 4) * 2),
+                           desc(ka + (i / 4) * 1024 + (i % 4) * 2), idesc_s, i > 0);
+            tc::mma_commit(&bar->s_full[me]);
+            tc::mma_commit(&bar->empty[at]);
+            if (held >= 0) tc::mma_commit(&bar->empty[held]);
+            held = -1;
+            if (j + 1 == n) tc::mma_commit(&bar->q_empty);
             return true;
         };
-        auto take = [&](int *at) {                       // the ring's next tile has landed
-            *at = ring.slot;
-            const bool ok = tc::mbar_wait(&bar->full[ring.slot], ring.phase, a.err, &bar->abort);
+        auto value = [&](int s, int j) {
+            const int at = ring.slot;
+            const uint32_t phase = ring.phase;
             ring.step(kSlots);
-            return ok;
-        };
-        auto checked = [&](int s, int j, int vs) {       // an edge tile's values are in order
-            if (!edge_tile(w, stream_a(w, s) + j)) return true;
-            const bool ok = tc::mbar_wait(&bar->fixed[vs], (fix_phase >> vs) & 1, a.err, &bar->abort);
-            fix_phase ^= 1u << vs;
-            return ok;
-        };
-        int ks = 0, vs = 0;
-        if (shared_keys(w)) {
-            const int n = max(w.n0, w.n1);
-            if (!take(&ks)) return;
-            if (w.n0 > 0) scores(0, ks);
-            if (w.n1 > 0) scores(1, ks);
-            tc::mma_commit(&bar->empty[ks]);
-            for (int j = 0; j < n; ++j) {
-                if (!take(&vs) || !checked(0, j, vs)) return;
-                bool have = false;
+            const bool edge = edge_tile(w, stream_a(w, s) + j);
+            const uint32_t fixed = (fix_phase >> at) & 1;
+            if (edge) fix_phase ^= 1u << at;
+            if (!tc::mbar_wait(&bar->full[at], phase, a.err, &bar->abort)) return false;
+            if (shared ? j >= n : s != me) {
+                tc::mbar_arrive(&bar->empty[at]);
+                return true;
+            }
+            if (edge && !tc::mbar_wait(&bar->fixed[at], fixed, a.err, &bar->abort)) return false;
+            // The next key tile is waited for here, and this value tile is
+            // released after the next scores, so that the scores follow the
+            // product without a pause: the softmax waits for them.
+            if (j + 1 < n) {
+                if (!tc::mbar_wait(&bar->full[ring.slot], ring.phase, a.err, &bar->abort)) return false;
+                seen = true;
+            }
+            const uint32_t va = desc_lo(sKV + at * kTile, 16384);
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (j < stream_n(w, s) && !values(s, j, vs)) return;
-                    if (j + 1 < n && !have) {
-                        if (!take(&ks)) return;
-                        have = true;
-                    }
-                    if (j + 1 < stream_n(w, s)) scores(s, ks);
-                }
-                tc::mma_commit(&bar->empty[vs]);
-                if (have) tc::mma_commit(&bar->empty[ks]);
+            for (int h = 0; h < 2; ++h) {                // P comes in two halves
+                if (!tc::mbar_wait(&bar->p_full[me][h], p_phase, a.err, &bar->abort)) return false;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int i = 4 * h; i < 4 * h + 4; ++i)
+                    tc::mma_ts(tO, tS + i * 8, desc(va + i * 128), idesc_o,
+                               (j > 0 || i > 0) ? 1u : 0u);
             }
-        } else {
-            for (int s = 0; s < 2; ++s) {
-                if (!take(&ks)) return;
-                scores(s, ks);
-                tc::mma_commit(&bar->empty[ks]);
+            p_phase ^= 1;
+            held = at;
+            if (j + 1 == n) {
+                tc::mma_commit(&bar->o_full[me]);
+                tc::mma_commit(&bar->empty[at]);
+                held = -1;
             }
-            for (int j = 0; j < w.n0; ++j)
-                for (int s = 0; s < 2; ++s) {
-                    const int n = stream_n(w, s);
-                    if (j >= n) continue;
-                    if (!take(&vs) || !checked(s, j, vs) || !values(s, j, vs)) return;
-                    tc::mma_commit(&bar->empty[vs]);
-                    if (j + 1 < n) {
-                        if (!take(&ks)) return;
-                        scores(s, ks);
-                        tc::mma_commit(&bar->empty[ks]);
-                    }
-                }
-        }
+            return true;
+        };
+        if (!for_tiles(w, key, value)) return;
     }
 }
 
 // ---------------------------------------------------------------- value check
 
-// Two warps.  In a tile that some row attends only in part, P is 0 at the
+// One warp.  In a tile that some row attends only in part, P is 0 at the
 // keys the row does not attend, and 0 times infinity or NaN would reach it:
 // rows of V that no row attends (other sequences, what a page held before)
 // are set to 0, and in rows that only later tokens attend, infinities and
@@ -379,7 +400,7 @@ __device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ,
 template <int D>
 __device__ void check_role(const TcArgs &a, Bars *bar, uint8_t *sKV) {
     constexpr int kSlots = ring_slots<D>(), kChunks = D / 8;
-    const int lane = threadIdx.x % 32, half = (threadIdx.x / 32) & 1;
+    const int lane = threadIdx.x % 32;
     Ring ring;
     uint32_t edge_phase = 0;                             // per slot
     for (int k = 0;; ++k) {
@@ -404,7 +425,7 @@ __device__ void check_role(const TcArgs &a, Bars *bar, uint8_t *sKV) {
                     uint8_t *base = sKV + ring.slot * (128 * D * 2);
                     const int from = max(0, w.pos0 + 1 - t * kFullKeys);
                     bool odd = false;
-                    for (int i = half * 32 + lane; i < (kFullKeys - from) * kChunks; i += 64) {
+                    for (int i = lane; i < (kFullKeys - from) * kChunks; i += 32) {
                         const int r = from + i / kChunks, ch = i % kChunks;
                         uint4 *p = (uint4 *)(base + (ch / 8) * 16384 + r * 128 +
                                              (((ch % 8) ^ (r & 7)) << 4));
@@ -464,6 +485,28 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+// 32 lanes x 16 consecutive 32-bit columns of TMEM.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// 32 bytes in one store of a whole sector where the tensor's base allows it
+// (`wide`: a multiple of 32), else in two.
+__device__ __forceinline__ void store32(void *dst, const uint32_t *v, bool wide) {
+    if (!wide) {
+        ((uint4 *)dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        ((uint4 *)dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+                   "r"(v[6]), "r"(v[7]) : "memory");
+}
 // max(a, b, c), NaN if one of them is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     float d;
@@ -497,77 +540,83 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
                  __uint_as_float(__float_as_uint(u) + (__float_as_uint(q) << 23)));
 }
 
-// The row's maximum over the attended columns of an S tile.
-template <bool kEdge>
-__device__ __forceinline__ float row_max(uint32_t tS, int lim) {
-    float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
-#pragma unroll 1
-    for (int h = 0; h < 128; h += 64) {
-        uint32_t v[64];
-        tc::tmem_ld32(tS + h, *(uint32_t(*)[32])v);
-        tc::tmem_ld32(tS + h + 32, *(uint32_t(*)[32])(v + 32));
-        tc::tmem_ld_wait();
-        if (kEdge) {
+// The row's maximum over an S tile's columns.
+__device__ __forceinline__ float row_max(const uint32_t (&v)[128]) {
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-                if (h + c > lim) v[c] = __float_as_uint(-INFINITY);
-        }
+    for (int c = 0; c < 128; c += 8)
 #pragma unroll
-        for (int c = 0; c < 64; c += 8) {
-            m0 = max3_nan(m0, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-            m1 = max3_nan(m1, __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
-            m2 = max3_nan(m2, __uint_as_float(v[c + 4]), __uint_as_float(v[c + 5]));
-            m3 = max3_nan(m3, __uint_as_float(v[c + 6]), __uint_as_float(v[c + 7]));
-        }
-    }
-    return max3_nan(max3_nan(m0, m1, m2), m3, m3);
+        for (int i = 0; i < 4; ++i)
+            m[i] = max3_nan(m[i], __uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1]));
+    return max3_nan(max3_nan(m[0], m[1], m[2]), m[3], m[3]);
 }
 
-#ifndef POLY
-#define POLY 5
-#endif
-// P = 2^(scale_log2 S - mb) of an S tile, as bf16 over the columns already
-// read; returns the fp32 row sum.  Every 32 columns, kPoly of the 16 pairs go
-// to the multiply-add pipe and the others to the special-function unit, which
-// alone would bound the kernel.
-template <bool kEdge>
-__device__ __forceinline__ float weights(uint32_t tS, int lim, float scale_log2, float mb) {
-    constexpr int kPoly = kEdge ? 0 : POLY;
-    const uint64_t scale2 = pack2(scale_log2, scale_log2), mb2 = pack2(-mb, -mb);
-    uint64_t l0 = 0, l1 = 0;                             // (0, 0)
+// The same two steps for a tile of which the row attends only columns up to
+// lim, in rolled loops over TMEM: rare, so kept small (the instruction cache
+// holds the softmax of whole tiles).
+__device__ __forceinline__ float edge_max(uint32_t tS, int lim) {
+    float m = -INFINITY;
 #pragma unroll 1
     for (int h = 0; h < 128; h += 32) {
+        uint32_t v[32];
+        tc::tmem_ld32(tS + h, v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 32; c += 2)
+            m = max3_nan(m, h + c > lim ? -INFINITY : __uint_as_float(v[c]),
+                         h + c + 1 > lim ? -INFINITY : __uint_as_float(v[c + 1]));
+    }
+    return m;
+}
+__device__ __forceinline__ float edge_weights(uint32_t tS, int from, int lim, float scale, float mb) {
+    float l = 0.f;
+#pragma unroll 1
+    for (int h = from; h < from + 64; h += 32) {
         uint32_t v[32], pk[16];
         tc::tmem_ld32(tS + h, v);
         tc::tmem_ld_wait();
-        if (kEdge) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-                if (h + c > lim) v[c] = __float_as_uint(-INFINITY);
-        }
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            uint64_t x2 = fma2(pack2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])),
-                               scale2, mb2);
-            float e0, e1;
-            if ((c + 1) * kPoly / 16 > c * kPoly / 16) {
-                x2 = exp2_poly2(x2);
-                unpack2(x2, e0, e1);
-            } else {
-                unpack2(x2, e0, e1);
-                e0 = tc::ex2_approx(e0);
-                e1 = tc::ex2_approx(e1);
-                x2 = pack2(e0, e1);
-            }
-            if (c & 1) l1 = add2(l1, x2); else l0 = add2(l0, x2);
+        for (int c = 0; c < 32; c += 2) {
+            const float e0 = h + c > lim ? 0.f : tc::ex2_approx(fmaf(__uint_as_float(v[c]), scale, mb));
+            const float e1 = h + c + 1 > lim ? 0.f : tc::ex2_approx(fmaf(__uint_as_float(v[c + 1]), scale, mb));
+            l += e0 + e1;
             __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
-            pk[c] = *(uint32_t *)&b;
+            pk[c / 2] = *(uint32_t *)&b;
         }
         tc::tmem_st16(tS + h / 2, pk);
     }
-    float a, b;
-    unpack2(add2(l0, l1), a, b);
-    return a + b;
+    return l;
+}
+
+#ifndef POLY
+#define POLY 4
+#endif
+// P = 2^(scale_log2 S - mb) of 32 columns, as bf16 over the S columns from tP
+// on; adds the fp32 row sum to l0, l1.  Of the 16 pairs kPoly go to the
+// multiply-add pipe, the others to the special-function unit.
+template <int kPoly, int kFrom>
+__device__ __forceinline__ void weights(const uint32_t (&v)[128], uint32_t tP, uint64_t scale2,
+                                        uint64_t mb2, uint64_t &l0, uint64_t &l1) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        uint64_t x2 = fma2(pack2(__uint_as_float(v[kFrom + 2 * c]),
+                                 __uint_as_float(v[kFrom + 2 * c + 1])), scale2, mb2);
+        float e0, e1;
+        if ((c + 1) * kPoly / 16 > c * kPoly / 16) {
+            x2 = exp2_poly2(x2);
+            unpack2(x2, e0, e1);
+        } else {
+            unpack2(x2, e0, e1);
+            e0 = tc::ex2_approx(e0);
+            e1 = tc::ex2_approx(e1);
+            x2 = pack2(e0, e1);
+        }
+        if (c & 1) l1 = add2(l1, x2); else l0 = add2(l0, x2);
+        __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
+        pk[c] = *(uint32_t *)&b;
+    }
+    tc::tmem_st16(tP + kFrom / 2, pk);
 }
 
 template <int D, bool kPaged>
@@ -577,33 +626,42 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
     const uint32_t tS = tmem + s * 128 + lane_off, tO = tmem + 256 + s * 128 + lane_off;
     const int row = quad * 32 + lane;
     const int tok = row / a.s.R, head = row % a.s.R;
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, turn_phase = 0;
+    const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     for (int k = 0;; ++k) {
         const int slot = k & 1;
         if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort)) return;
-        const Item w = bar->item[slot];
+        const Item &w = bar->item[slot];                 // read where needed: registers are short
         if (!w.valid) return;
         const int first_tok = w.pair ? s * a.c.half_tokens : 0;
         const int toks = min(a.c.half_tokens, w.nt - first_tok);
         const bool valid = tok < toks;
         const bool busy = quad * 32 < toks * a.s.R;      // the warp holds a row
-        const int pos = w.pos0 + first_tok + tok;
+        const int first_pos = w.pos0 + first_tok;        // of the stream's first token
         const int t0 = stream_a(w, s), n = stream_n(w, s);
+        // The two streams' warps on one scheduler take turns at the
+        // exponentials, first stream 0's, while both have tiles and rows: each then
+        // runs its exponentials beside the other's products.  Left alone the
+        // streams fall into step, and wait for the same unit at the same time.
+        const int other = w.pair ? min(a.c.half_tokens, w.nt - (s ? 0 : a.c.half_tokens)) : toks;
+        const int turns = quad * 32 < min(toks, other) * a.s.R ? min(w.n0, w.n1) : 0;
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < n; ++j) {
             if (!tc::mbar_wait(&bar->s_full[s], s_phase, a.err, &bar->abort)) return;
             s_phase ^= 1;
-            if (busy) {
-                tc::tc_fence_after();
-                const int key0 = (t0 + j) * kFullKeys;
-                // columns above lim are not attended by this row
-                const bool edge = key0 + kFullKeys > w.pos0 + first_tok + 1;
-                const int lim = edge ? pos - key0 : kFullKeys;
-                float top = edge ? row_max<true>(tS, lim) : row_max<false>(tS, lim);
-                // S(j) is complete, and with it (one thread issues both, in
-                // order) the product P V of tile j - 1: O may be rescaled.
-                // Not "top > m + lag", so that a NaN moves m too.
-                const bool move = !(top <= m + a.lag);
+            const int key0 = (t0 + j) * kFullKeys;
+            if (!busy) {
+                arrive_if(lane == 0, &bar->p_full[s][0]);
+                arrive_if(lane == 0, &bar->p_full[s][1]);
+                continue;
+            }
+            tc::tc_fence_after();
+            // The row's maximum in this tile is known: move m, and O with it.
+            // S(j) is complete, and with it (one thread issues both, in order)
+            // the product P V of tile j - 1, so O may be rescaled.  Returns
+            // -m scale log2(e).
+            auto moved = [&](float top) {
+                const bool move = !(top <= m + a.lag);   // (a NaN moves m too)
                 if (j == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, move)) {
@@ -611,25 +669,62 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                     if (move) m = top;
                     l *= f;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tc::tmem_ld32(tO + c, o);
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + c, o);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < 16; ++i)
                             o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tc::tmem_st32(tO + c, o);
+                        tc::tmem_st16(tO + c, o);
                     }
                 }
-                const float mb = m == -INFINITY ? 0.f : m * a.scale_log2;
-                const float sum = edge ? weights<true>(tS, lim, a.scale_log2, mb)
-                                       : weights<false>(tS, lim, a.scale_log2, mb);
-                if (m != -INFINITY) l += sum;            // (a row of -inf scores has no weight)
+                return m == -INFINITY ? 0.f : -m * a.scale_log2;
+            };
+            auto my_turn = [&]() {                       // (stream 0's very first turn is free)
+                if (j >= turns) return true;
+                const uint32_t phase = turn_phase ^ (s ^ 1);
+                turn_phase ^= 1;
+                return tc::mbar_wait(&bar->turn[s][quad], phase, a.err, &bar->abort);
+            };
+            auto half_done = [&](int h) {                // 64 keys' weights are in TMEM
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
+                __syncwarp();
+                arrive_if(lane == 0, &bar->p_full[s][h]);
+            };
+            float sum;
+            if (key0 + kFullKeys > first_pos + 1) {
+                const int lim = first_pos + tok - key0;  // columns above lim are not attended
+                const float mb = moved(edge_max(tS, lim));
+                if (!my_turn()) return;
+                sum = edge_weights(tS, 0, lim, a.scale_log2, mb);
+                half_done(0);
+                sum += edge_weights(tS, 64, lim, a.scale_log2, mb);
+                arrive_if(lane == 0 && j < turns, &bar->turn[1 - s][quad]);
+            } else {
+                uint32_t v[128];
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) tc::tmem_ld32(tS + c, *(uint32_t(*)[32])(v + c));
+                tc::tmem_ld_wait();
+                const float mb = moved(row_max(v));
+                const uint64_t mb2 = pack2(mb, mb);
+                uint64_t l0 = 0, l1 = 0;                 // (0, 0)
+                if (!my_turn()) return;
+                weights<POLY, 0>(v, tS, scale2, mb2, l0, l1);
+                weights<POLY, 32>(v, tS, scale2, mb2, l0, l1);
+                half_done(0);
+                weights<POLY, 64>(v, tS, scale2, mb2, l0, l1);
+                // (the turn is handed over a little early: the other warp
+                // needs ~190 cycles to see it)
+                arrive_if(lane == 0 && j < turns, &bar->turn[1 - s][quad]);
+                weights<POLY, 96>(v, tS, scale2, mb2, l0, l1);
+                float x, y;
+                unpack2(add2(l0, l1), x, y);
+                sum = x + y;
             }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bar->p_full[s]);
+            if (m != -INFINITY) l += sum;                // (a row of -inf scores has no weight)
+            half_done(1);
         }
         // epilogue: O / l and the log-sum-exp, final or as one of the row's parts
         if (n > 0) {
@@ -662,7 +757,7 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                     for (int i = 0; i < 32; ++i)
                         x[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
                     if (odd && valid) {
-                        const int hi = min(pos, (t0 + n) * kFullKeys - 1);
+                        const int hi = min(first_pos + tok, (t0 + n) * kFullKeys - 1);
                         for (int jk = max(t0 * kFullKeys, w.pos0 + 1); jk <= hi; ++jk) {
                             int64_t kr = (int64_t)w.k0 + jk;
                             if (kPaged)
@@ -678,20 +773,20 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                         }
                     }
                     if (valid && w.parts > 0) {
-                        float4 *dst = (float4 *)(a.part_o + part * D + c);
+                        float *dst = a.part_o + part * D + c;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            dst[i / 4] = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        for (int i = 0; i < 32; i += 8) store32(dst + i, (const uint32_t *)(x + i), true);
                     } else if (valid) {
-                        uint4 *dst = (uint4 *)(a.O + at * D + c);
+                        __nv_bfloat16 *dst = a.O + at * D + c;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint4 u;
-                            __nv_bfloat162 *h = (__nv_bfloat162 *)&u;
+                        for (int i = 0; i < 32; i += 16) {
+                            uint32_t u[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                h[e] = __floats2bfloat162_rn(x[i + 2 * e], x[i + 2 * e + 1]);
-                            dst[i / 8] = u;
+                            for (int e = 0; e < 8; ++e) {
+                                __nv_bfloat162 h = __floats2bfloat162_rn(x[i + 2 * e], x[i + 2 * e + 1]);
+                                u[e] = *(uint32_t *)&h;
+                            }
+                            store32(dst + i, u, a.wide);
                         }
                     }
                 }
@@ -717,18 +812,20 @@ full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
             tc::mbar_init(&bar->full[i], 1);
-            tc::mbar_init(&bar->empty[i], 1);
+            tc::mbar_init(&bar->empty[i], 2);            // one per stream
             tc::mbar_init(&bar->issued[i], 1);
-            tc::mbar_init(&bar->fixed[i], 2);
+            tc::mbar_init(&bar->fixed[i], 1);
         }
         tc::mbar_init(&bar->q_full, 1);
-        tc::mbar_init(&bar->q_empty, 1);
+        tc::mbar_init(&bar->q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bar->s_full[i], 1);
-            tc::mbar_init(&bar->p_full[i], 4);           // one per softmax warp
+            tc::mbar_init(&bar->p_full[i][0], 4);        // one per softmax warp
+            tc::mbar_init(&bar->p_full[i][1], 4);
             tc::mbar_init(&bar->o_full[i], 1);
+            for (int q = 0; q < 4; ++q) tc::mbar_init(&bar->turn[i][q], 1);
             tc::mbar_init(&bar->item_full[i], 1);
-            tc::mbar_init(&bar->item_empty[i], 1 + 2 + 8);   // MMA, check and softmax warps
+            tc::mbar_init(&bar->item_empty[i], 2 + 1 + 8);   // MMA, check and softmax warps
             bar->odd[i] = 0;
         }
         bar->abort = 0;
@@ -742,10 +839,9 @@ full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     if (warp < 4) {
         tc::regs_dec<kRegsLoad>();
         if (warp == 0) load_role<D, kPaged>(a, bar, sQ, sKV, &tm_q, &tm_k, &tm_v);
-        else if (warp == 1) {
-            if (threadIdx.x % 32 == 0)
-                mma_role<D>(a, bar, tmem, tc::smem_u32(sQ), tc::smem_u32(sKV));
-        } else check_role<D>(a, bar, sKV);
+        else if (warp == 3) check_role<D>(a, bar, sKV);
+        else if (threadIdx.x % 32 == 0)
+            mma_role<D>(a, bar, tmem, tc::smem_u32(sQ), tc::smem_u32(sKV), warp - 1);
     } else {
         tc::regs_inc<kRegsSoftmax>();
         softmax_role<D, kPaged>(a, bar, tmem, warp / 4 - 1);
@@ -821,6 +917,7 @@ cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut 
     a.V = (const __nv_bfloat16 *)V;
     a.O = (__nv_bfloat16 *)O;
     a.lse = lse; a.part_o = part_o; a.part_lse = part_lse; a.err = err;
+    a.wide = ((uintptr_t)O & 31u) == 0;
     a.scale_log2 = s.scale * kLog2e;
     a.lag = kMaxLag / a.scale_log2;
     a.box = kFullKeys;                   // the largest power of two that divides pages and tiles
