@@ -6,14 +6,22 @@
 // A row tile is 128 (token, head of the KV group) rows: 128 / R tokens with
 // their R query heads, so that K and V are read once for the group.  A CTA
 // holds two of them in flight (streams 0 and 1), each with its own softmax
-// warpgroup, so that the tensor cores work on one while the other is in its
-// softmax.  A unit of work is two row tiles of consecutive tokens against the
-// same keys; one of at most 128 / R tokens (decode, ends of prompts) is a
-// single row tile whose key run the two streams share half and half.
+// warpgroup and its own product-issuing thread.  A unit of work is two row
+// tiles of consecutive tokens against the same keys; one of at most 128 / R
+// tokens (decode, ends of prompts) is a single row tile whose key run the two
+// streams share half and half.
 //
 //   S = Q K^T      tcgen05, operands from shared memory, fp32 in TMEM
 //   P = 2^(scale log2(e) (S - m))    in registers, bf16 over S in TMEM
 //   O += P V       tcgen05, P from TMEM, O (fp32) in TMEM
+//
+// K and V come in tiles of 128 keys; S and P go in halves of 64, two buffers
+// a stream (TMEM: streams' buffers in columns 0, 64 and 128, 192; O in 256
+// and 384), so that the scores of the next half are ready when the softmax of
+// this one ends.  With one 128-key buffer a stream (all that fits beside O)
+// every softmax waited for the product before it, the scores after it and two
+// hand-overs, 1400 of 3800 cycles a tile, while neither the tensor cores nor
+// the special-function units were half busy.
 //
 // The running maximum m a row's P is taken against moves only when a tile's
 // maximum passes it by more than 2^8: P stays below 2^8 (the same relative
@@ -34,8 +42,7 @@ constexpr int kThreads = 384;            // loads + MMA + value check, two softm
 constexpr int kRows = 128;               // rows of a row tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxLag = 8.f;           // log2 of how far P may pass 1
-constexpr int kRegsLoad = 88, kRegsSoftmax = 208;
-static_assert(kRegsLoad + 2 * kRegsSoftmax <= 3 * 168, "register budgets exceed the launch's");
+constexpr int kHalf = 64;                // keys of one S / P buffer
 
 template <int D> constexpr int ring_slots() { return D == 128 ? 5 : 10; }
 template <int D> constexpr size_t tc_smem() {
@@ -62,14 +69,15 @@ struct TcArgs {
 struct Item {
     int valid, b, g, q0;                 // q0: row of Q of the unit's first token
     int nt, pos0, k0, pair;              // tokens; position of the first; packed key row 0
-    int a0, a1, n0, n1;                  // each stream's first key tile and their number
+    int a0, a1, h0, h1;                  // each stream's first key tile and number of halves
     int part, parts, pad0, pad1;         // key run, and how many the rows' results come in
 };
 
 __device__ __forceinline__ int stream_a(const Item &w, int s) { return s ? w.a1 : w.a0; }
-__device__ __forceinline__ int stream_n(const Item &w, int s) { return s ? w.n1 : w.n0; }
+__device__ __forceinline__ int stream_h(const Item &w, int s) { return s ? w.h1 : w.h0; }
+__device__ __forceinline__ int stream_n(const Item &w, int s) { return (stream_h(w, s) + 1) / 2; }
 // The streams read the same key tiles (a pair of row tiles, or one stream idle).
-__device__ __forceinline__ bool shared_keys(const Item &w) { return w.pair || w.n1 == 0; }
+__device__ __forceinline__ bool shared_keys(const Item &w) { return w.pair || w.h1 == 0; }
 // Some row of the unit does not attend all of key tile t.
 __device__ __forceinline__ bool edge_tile(const Item &w, int t) {
     return (t + 1) * kFullKeys > w.pos0 + 1;
@@ -92,23 +100,24 @@ __device__ __forceinline__ Item make_item(const TcArgs &a, const FullSeq &q, int
     w.pair = w.nt > a.c.half_tokens;
     w.parts = full_row_parts(q, a.c, t0);
     const int lo = w.part * q.tiles;
-    auto run = [&](int tokens) {         // key tiles of this part that the first tokens see
-        const int seen = (max(0, w.pos0 + tokens) + kFullKeys - 1) / kFullKeys;
-        return max(0, min(seen, lo + q.tiles) - lo);
+    auto run = [&](int tokens) {         // halves of this part that the first tokens see
+        const int seen = (max(0, w.pos0 + tokens) + kHalf - 1) / kHalf;
+        return max(0, min(seen, 2 * (lo + q.tiles)) - 2 * lo);
     };
-    const int n = run(w.nt);
+    const int h = run(w.nt);
     w.a0 = w.a1 = lo;
     if (w.pair) {
-        w.n0 = run(a.c.half_tokens);
-        w.n1 = n;
+        w.h0 = run(a.c.half_tokens);
+        w.h1 = h;
     } else if (a.c.max_parts > 1) {
-        w.n0 = (n + 1) / 2;
-        w.n1 = n - w.n0;
-        w.a1 = lo + w.n0;
+        const int tiles = ((h + 1) / 2 + 1) / 2;         // the first half of the tiles
+        w.h0 = min(h, 2 * tiles);
+        w.h1 = h - w.h0;
+        w.a1 = lo + tiles;
         w.part *= 2;
     } else {
-        w.n0 = n;
-        w.n1 = 0;
+        w.h0 = h;
+        w.h1 = 0;
     }
     return w;
 }
@@ -118,7 +127,7 @@ struct Bars {
     // was issued (the check warps skip the other tiles, so they cannot follow
     // `full` by its phases alone); an edge tile's values are in order
     uint64_t full[10], empty[10], issued[10], fixed[10];
-    uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], turn[2][4], item_full[2], item_empty[2];
+    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_prev[2], o_full[2], item_full[2], item_empty[2];
     Item item[2];
     volatile int odd[2];                 // item count + 1 where an edge tile held inf or NaN
     uint32_t tmem;
@@ -128,8 +137,7 @@ static_assert(sizeof(Bars) <= 1024, "barrier block");
 
 // One lane's arrival, without a branch and without the release fence of a
 // plain arrival (together about 150 cycles of a softmax tile).  What it
-// announces is in TMEM, ordered by tcgen05.wait::st and the fences around it,
-// or nothing but the turn itself.
+// announces is in TMEM, ordered by tcgen05.wait::st and the fences around it.
 __device__ __forceinline__ void arrive_if(bool pred, uint64_t *bar) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
@@ -154,8 +162,9 @@ struct Ring {
 // keys are shared); false as soon as one of them fails.
 template <typename FK, typename FV>
 __device__ __forceinline__ bool for_tiles(const Item &w, FK k, FV v) {
+    const int n0 = stream_n(w, 0), n1 = stream_n(w, 1);
     if (shared_keys(w)) {
-        const int n = max(w.n0, w.n1);
+        const int n = max(n0, n1);
         if (n > 0 && !k(0, 0)) return false;
         for (int j = 0; j < n; ++j) {
             if (!v(0, j)) return false;
@@ -164,9 +173,9 @@ __device__ __forceinline__ bool for_tiles(const Item &w, FK k, FV v) {
         return true;
     }
     if (!k(0, 0) || !k(1, 0)) return false;              // both streams have a tile
-    for (int j = 0; j < w.n0; ++j)                        // n0 >= n1
+    for (int j = 0; j < n0; ++j)                          // n0 >= n1
         for (int s = 0; s < 2; ++s) {
-            const int n = stream_n(w, s);
+            const int n = s ? n1 : n0;
             if (j < n && !v(s, j)) return false;
             if (j + 1 < n && !k(s, j + 1)) return false;
         }
@@ -205,7 +214,7 @@ __device__ void load_role(const TcArgs &a, Bars *bar, uint8_t *sQ, uint8_t *sKV,
             tc::mbar_arrive(&bar->item_full[slot]);
         }
         if (!w.valid) break;
-        if (w.n0 + w.n1 > 0) {
+        if (w.h0 + w.h1 > 0) {
             if (!tc::mbar_wait(&bar->q_empty, (q_uses & 1) ^ 1, a.err, &bar->abort)) break;
             ++q_uses;
             const int tiles = w.pair ? 2 : 1;
@@ -291,20 +300,24 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo) {
     return d;
 }
 
-// One thread issues the products of one stream.  The two streams' threads sit
-// in different warps and do not wait for each other: with one thread for both,
-// its waits and commits (about 900 cycles a tile) were the kernel's bound.
+// One thread issues the products of one stream: S(0), S(1), then for each half
+// i, once its P is there, O += P(i) V(i) and S(i + 2), which takes the buffer
+// P(i) was in.  The two streams' threads sit in different warps and do not
+// wait for each other: with one thread for both, its waits and commits (900
+// cycles a tile) were the kernel's bound.  S of 64 keys runs at 49 cycles a
+// product (its operands come from shared memory at 128 bytes a clock) where
+// 32 would be ideal, which the other stream's products partly fill.
 template <int D>
 __device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ, uint32_t sKV,
                          int me) {
     constexpr int kSlots = ring_slots<D>();
     constexpr uint32_t kTile = 128 * D * 2;
-    constexpr uint32_t idesc_s = tc::idesc_bf16(kRows, kFullKeys, 0, 0);
+    constexpr uint32_t idesc_s = tc::idesc_bf16(kRows, kHalf, 0, 0);
     constexpr uint32_t idesc_o = tc::idesc_bf16(kRows, D, 0, 1);
     const uint32_t tS = tmem + me * 128, tO = tmem + 256 + me * 128;
     Ring ring;
     uint32_t fix_phase = 0;                              // per slot
-    uint32_t p_phase = 0;
+    uint32_t p_phase = 0;                                // per buffer
     int q_uses = 0;
     for (int k = 0;; ++k) {
         const int slot = k & 1;
@@ -312,39 +325,54 @@ __device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ,
         const Item w = bar->item[slot];
         tc::mbar_arrive(&bar->item_empty[slot]);
         if (!w.valid) return;
-        if (w.n0 + w.n1 == 0) continue;
+        if (w.h0 + w.h1 == 0) continue;
         if (!tc::mbar_wait(&bar->q_full, q_uses & 1, a.err, &bar->abort)) return;
         ++q_uses;
         const bool shared = shared_keys(w);
-        const int n = stream_n(w, me);
-        if (n == 0) tc::mbar_arrive(&bar->q_empty);
+        const int h = stream_h(w, me), n = (h + 1) / 2;
+        if (h == 0) tc::mbar_arrive(&bar->q_empty);
         const uint32_t qa = desc_lo(sQ + (w.pair && me ? kTile : 0), 16);
         // Both threads wait for every tile and release every tile, so that
         // neither can be a lap of the ring ahead of the other (a phase's
         // parity tells one lap only).
-        int held = -1;                                   // a value slot not yet released
-        bool seen = false;                               // the next key tile was waited for
+        auto scores = [&](int i, uint32_t k_tile) {      // half i, of the key tile at k_tile
+            const uint32_t ka = desc_lo(k_tile, 16) + (i & 1) * 512;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c)
+                tc::mma_ss(tS + (i & 1) * kHalf, desc(qa + (c / 4) * 1024 + (c % 4) * 2),
+                           desc(ka + (c / 4) * 1024 + (c % 4) * 2), idesc_s, c > 0);
+            tc::mma_commit(&bar->s_full[me][i & 1]);
+            if (i + 1 == h) tc::mma_commit(&bar->q_empty);
+        };
+        auto product = [&](int i, uint32_t va) {         // half i, of the value tile at va
+            const int b = i & 1;
+            if (!tc::mbar_wait(&bar->p_full[me][b], (p_phase >> b) & 1, a.err, &bar->abort))
+                return false;
+            p_phase ^= 1u << b;
+            tc::tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kHalf / 16; ++c)
+                tc::mma_ts(tO, tS + b * kHalf + c * 8, desc(va + (b * 4 + c) * 128), idesc_o,
+                           (i > 0 || c > 0) ? 1u : 0u);
+            if (i + 2 == h) tc::mma_commit(&bar->o_prev[me]);
+            if (i + 1 == h) tc::mma_commit(&bar->o_full[me]);
+            return true;
+        };
         auto key = [&](int s, int j) {
             const int at = ring.slot;
             const uint32_t phase = ring.phase;
             ring.step(kSlots);
-            if (!seen && !tc::mbar_wait(&bar->full[at], phase, a.err, &bar->abort)) return false;
-            seen = false;
-            if (shared ? j >= n : s != me) {
+            const bool mine = shared ? j < n : s == me;
+            if (mine && j > 0) return true;              // its scores went with the values before
+            if (!tc::mbar_wait(&bar->full[at], phase, a.err, &bar->abort)) return false;
+            if (!mine) {
                 tc::mbar_arrive(&bar->empty[at]);
                 return true;
             }
-            const uint32_t ka = desc_lo(sKV + at * kTile, 16);
             tc::tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                tc::mma_ss(tS, desc(qa + (i / 4) * 1024 + (i % 4) * 2),
-                           desc(ka + (i / 4) * 1024 + (i % 4) * 2), idesc_s, i > 0);
-            tc::mma_commit(&bar->s_full[me]);
+            scores(0, sKV + at * kTile);
+            if (h > 1) scores(1, sKV + at * kTile);
             tc::mma_commit(&bar->empty[at]);
-            if (held >= 0) tc::mma_commit(&bar->empty[held]);
-            held = -1;
-            if (j + 1 == n) tc::mma_commit(&bar->q_empty);
             return true;
         };
         auto value = [&](int s, int j) {
@@ -355,35 +383,22 @@ __device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ,
             const uint32_t fixed = (fix_phase >> at) & 1;
             if (edge) fix_phase ^= 1u << at;
             if (!tc::mbar_wait(&bar->full[at], phase, a.err, &bar->abort)) return false;
-            if (shared ? j >= n : s != me) {
+            if (!(shared ? j < n : s == me)) {
                 tc::mbar_arrive(&bar->empty[at]);
                 return true;
             }
             if (edge && !tc::mbar_wait(&bar->fixed[at], fixed, a.err, &bar->abort)) return false;
-            // The next key tile is waited for here, and this value tile is
-            // released after the next scores, so that the scores follow the
-            // product without a pause: the softmax waits for them.
-            if (j + 1 < n) {
-                if (!tc::mbar_wait(&bar->full[ring.slot], ring.phase, a.err, &bar->abort)) return false;
-                seen = true;
-            }
             const uint32_t va = desc_lo(sKV + at * kTile, 16384);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {                // P comes in two halves
-                if (!tc::mbar_wait(&bar->p_full[me][h], p_phase, a.err, &bar->abort)) return false;
-                tc::tc_fence_after();
-#pragma unroll
-                for (int i = 4 * h; i < 4 * h + 4; ++i)
-                    tc::mma_ts(tO, tS + i * 8, desc(va + i * 128), idesc_o,
-                               (j > 0 || i > 0) ? 1u : 0u);
+            const int next = ring.slot;                  // the next key tile follows in the ring
+            if (!product(2 * j, va)) return false;
+            if (2 * j + 2 < h) {
+                if (!tc::mbar_wait(&bar->full[next], ring.phase, a.err, &bar->abort)) return false;
+                scores(2 * j + 2, sKV + next * kTile);
             }
-            p_phase ^= 1;
-            held = at;
-            if (j + 1 == n) {
-                tc::mma_commit(&bar->o_full[me]);
-                tc::mma_commit(&bar->empty[at]);
-                held = -1;
-            }
+            if (2 * j + 1 < h && !product(2 * j + 1, va)) return false;
+            tc::mma_commit(&bar->empty[at]);
+            if (2 * j + 3 < h) scores(2 * j + 3, sKV + next * kTile);
+            if (2 * j + 2 < h) tc::mma_commit(&bar->empty[next]);
             return true;
         };
         if (!for_tiles(w, key, value)) return;
@@ -485,16 +500,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// 32 lanes x 16 consecutive 32-bit columns of TMEM.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
 // 32 bytes in one store of a whole sector where the tensor's base allows it
 // (`wide`: a multiple of 32), else in two.
 __device__ __forceinline__ void store32(void *dst, const uint32_t *v, bool wide) {
@@ -540,83 +545,53 @@ __device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
                  __uint_as_float(__float_as_uint(u) + (__float_as_uint(q) << 23)));
 }
 
-// The row's maximum over an S tile's columns.
-__device__ __forceinline__ float row_max(const uint32_t (&v)[128]) {
+// The maximum of a row's 64 scores.
+__device__ __forceinline__ float row_max(const uint32_t (&v)[kHalf]) {
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int c = 0; c < 128; c += 8)
+    for (int c = 0; c < kHalf; c += 8)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             m[i] = max3_nan(m[i], __uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1]));
     return max3_nan(max3_nan(m[0], m[1], m[2]), m[3], m[3]);
 }
 
-// The same two steps for a tile of which the row attends only columns up to
-// lim, in rolled loops over TMEM: rare, so kept small (the instruction cache
-// holds the softmax of whole tiles).
-__device__ __forceinline__ float edge_max(uint32_t tS, int lim) {
-    float m = -INFINITY;
-#pragma unroll 1
-    for (int h = 0; h < 128; h += 32) {
-        uint32_t v[32];
-        tc::tmem_ld32(tS + h, v);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 32; c += 2)
-            m = max3_nan(m, h + c > lim ? -INFINITY : __uint_as_float(v[c]),
-                         h + c + 1 > lim ? -INFINITY : __uint_as_float(v[c + 1]));
-    }
-    return m;
-}
-__device__ __forceinline__ float edge_weights(uint32_t tS, int from, int lim, float scale, float mb) {
-    float l = 0.f;
-#pragma unroll 1
-    for (int h = from; h < from + 64; h += 32) {
-        uint32_t v[32], pk[16];
-        tc::tmem_ld32(tS + h, v);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-            const float e0 = h + c > lim ? 0.f : tc::ex2_approx(fmaf(__uint_as_float(v[c]), scale, mb));
-            const float e1 = h + c + 1 > lim ? 0.f : tc::ex2_approx(fmaf(__uint_as_float(v[c + 1]), scale, mb));
-            l += e0 + e1;
-            __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
-            pk[c / 2] = *(uint32_t *)&b;
-        }
-        tc::tmem_st16(tS + h / 2, pk);
-    }
-    return l;
-}
-
 #ifndef POLY
 #define POLY 4
 #endif
-// P = 2^(scale_log2 S - mb) of 32 columns, as bf16 over the S columns from tP
-// on; adds the fp32 row sum to l0, l1.  Of the 16 pairs kPoly go to the
-// multiply-add pipe, the others to the special-function unit.
-template <int kPoly, int kFrom>
-__device__ __forceinline__ void weights(const uint32_t (&v)[128], uint32_t tP, uint64_t scale2,
-                                        uint64_t mb2, uint64_t &l0, uint64_t &l1) {
-    uint32_t pk[16];
+// P = 2^(scale_log2 S - mb) of a half, as bf16 over S; returns the fp32 row
+// sum.  Of each 16 pairs kPoly go to the multiply-add pipe, the others to the
+// special-function unit.
+template <int kPoly>
+__device__ __forceinline__ float weights(const uint32_t (&v)[kHalf], uint32_t tP, uint64_t scale2,
+                                         uint64_t mb2) {
+    uint64_t l0 = 0, l1 = 0;                             // (0, 0)
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        uint64_t x2 = fma2(pack2(__uint_as_float(v[kFrom + 2 * c]),
-                                 __uint_as_float(v[kFrom + 2 * c + 1])), scale2, mb2);
-        float e0, e1;
-        if ((c + 1) * kPoly / 16 > c * kPoly / 16) {
-            x2 = exp2_poly2(x2);
-            unpack2(x2, e0, e1);
-        } else {
-            unpack2(x2, e0, e1);
-            e0 = tc::ex2_approx(e0);
-            e1 = tc::ex2_approx(e1);
-            x2 = pack2(e0, e1);
+    for (int h = 0; h < kHalf; h += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            uint64_t x2 = fma2(pack2(__uint_as_float(v[h + 2 * c]), __uint_as_float(v[h + 2 * c + 1])),
+                               scale2, mb2);
+            float e0, e1;
+            if ((c + 1) * kPoly / 16 > c * kPoly / 16) {
+                x2 = exp2_poly2(x2);
+                unpack2(x2, e0, e1);
+            } else {
+                unpack2(x2, e0, e1);
+                e0 = tc::ex2_approx(e0);
+                e1 = tc::ex2_approx(e1);
+                x2 = pack2(e0, e1);
+            }
+            if (c & 1) l1 = add2(l1, x2); else l0 = add2(l0, x2);
+            __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
+            pk[c] = *(uint32_t *)&b;
         }
-        if (c & 1) l1 = add2(l1, x2); else l0 = add2(l0, x2);
-        __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
-        pk[c] = *(uint32_t *)&b;
+        tc::tmem_st16(tP + h / 2, pk);
     }
-    tc::tmem_st16(tP + kFrom / 2, pk);
+    float x, y;
+    unpack2(add2(l0, l1), x, y);
+    return x + y;
 }
 
 template <int D, bool kPaged>
@@ -626,7 +601,7 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
     const uint32_t tS = tmem + s * 128 + lane_off, tO = tmem + 256 + s * 128 + lane_off;
     const int row = quad * 32 + lane;
     const int tok = row / a.s.R, head = row % a.s.R;
-    uint32_t s_phase = 0, o_phase = 0, turn_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, prev_phase = 0;   // s_phase: per buffer
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     for (int k = 0;; ++k) {
         const int slot = k & 1;
@@ -638,100 +613,71 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
         const bool valid = tok < toks;
         const bool busy = quad * 32 < toks * a.s.R;      // the warp holds a row
         const int first_pos = w.pos0 + first_tok;        // of the stream's first token
-        const int t0 = stream_a(w, s), n = stream_n(w, s);
-        // The two streams' warps on one scheduler take turns at the
-        // exponentials, first stream 0's, while both have tiles and rows: each then
-        // runs its exponentials beside the other's products.  Left alone the
-        // streams fall into step, and wait for the same unit at the same time.
-        const int other = w.pair ? min(a.c.half_tokens, w.nt - (s ? 0 : a.c.half_tokens)) : toks;
-        const int turns = quad * 32 < min(toks, other) * a.s.R ? min(w.n0, w.n1) : 0;
+        const int t0 = stream_a(w, s), h = stream_h(w, s), n = (h + 1) / 2;
         float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < n; ++j) {
-            if (!tc::mbar_wait(&bar->s_full[s], s_phase, a.err, &bar->abort)) return;
-            s_phase ^= 1;
-            const int key0 = (t0 + j) * kFullKeys;
-            if (!busy) {
-                arrive_if(lane == 0, &bar->p_full[s][0]);
-                arrive_if(lane == 0, &bar->p_full[s][1]);
-                continue;
-            }
-            tc::tc_fence_after();
-            // The row's maximum in this tile is known: move m, and O with it.
-            // S(j) is complete, and with it (one thread issues both, in order)
-            // the product P V of tile j - 1, so O may be rescaled.  Returns
-            // -m scale log2(e).
-            auto moved = [&](float top) {
-                const bool move = !(top <= m + a.lag);   // (a NaN moves m too)
-                if (j == 0) {
+        for (int i = 0; i < h; ++i) {
+            const int b = i & 1;
+            const uint32_t tB = tS + b * kHalf;
+            if (!tc::mbar_wait(&bar->s_full[s][b], (s_phase >> b) & 1, a.err, &bar->abort)) return;
+            s_phase ^= 1u << b;
+            if (busy) {
+                tc::tc_fence_after();
+                uint32_t v[kHalf];
+                tc::tmem_ld32(tB, *(uint32_t(*)[32])v);
+                tc::tmem_ld32(tB + 32, *(uint32_t(*)[32])(v + 32));
+                tc::tmem_ld_wait();
+                const int key0 = t0 * kFullKeys + i * kHalf;
+                const bool edge = key0 + kHalf > first_pos + 1;
+                if (edge) {
+                    const int lim = first_pos + tok - key0;   // columns above lim are not attended
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c)
+                        if (c > lim) v[c] = __float_as_uint(-INFINITY);
+                }
+                const float top = row_max(v);
+                const bool move = valid && !(top <= m + a.lag);   // (a NaN moves m too)
+                if (i == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, move)) {
+                    // O is rescaled between the products of halves i - 1 and
+                    // i.  The first is complete once S(i + 1), issued after
+                    // it, is; at the last half o_prev tells.
+                    if (i + 1 < h ? !tc::mbar_wait(&bar->s_full[s][b ^ 1], (s_phase >> (b ^ 1)) & 1,
+                                                   a.err, &bar->abort)
+                                  : !tc::mbar_wait(&bar->o_prev[s], prev_phase, a.err, &bar->abort))
+                        return;
+                    tc::tc_fence_after();
                     const float f = move ? tc::ex2_approx((m - top) * a.scale_log2) : 1.f;
                     if (move) m = top;
                     l *= f;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(tO + c, o);
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(tO + c, o);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tc::tmem_st16(tO + c, o);
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc::tmem_st32(tO + c, o);
                     }
                 }
-                return m == -INFINITY ? 0.f : -m * a.scale_log2;
-            };
-            auto my_turn = [&]() {                       // (stream 0's very first turn is free)
-                if (j >= turns) return true;
-                const uint32_t phase = turn_phase ^ (s ^ 1);
-                turn_phase ^= 1;
-                return tc::mbar_wait(&bar->turn[s][quad], phase, a.err, &bar->abort);
-            };
-            auto half_done = [&](int h) {                // 64 keys' weights are in TMEM
+                const float mb = m == -INFINITY ? 0.f : -m * a.scale_log2;
+                const float sum = edge ? weights<0>(v, tB, scale2, pack2(mb, mb))
+                                       : weights<POLY>(v, tB, scale2, pack2(mb, mb));
+                if (m != -INFINITY) l += sum;            // (a row of -inf scores has no weight)
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
-                __syncwarp();
-                arrive_if(lane == 0, &bar->p_full[s][h]);
-            };
-            float sum;
-            if (key0 + kFullKeys > first_pos + 1) {
-                const int lim = first_pos + tok - key0;  // columns above lim are not attended
-                const float mb = moved(edge_max(tS, lim));
-                if (!my_turn()) return;
-                sum = edge_weights(tS, 0, lim, a.scale_log2, mb);
-                half_done(0);
-                sum += edge_weights(tS, 64, lim, a.scale_log2, mb);
-                arrive_if(lane == 0 && j < turns, &bar->turn[1 - s][quad]);
-            } else {
-                uint32_t v[128];
-#pragma unroll
-                for (int c = 0; c < 128; c += 32) tc::tmem_ld32(tS + c, *(uint32_t(*)[32])(v + c));
-                tc::tmem_ld_wait();
-                const float mb = moved(row_max(v));
-                const uint64_t mb2 = pack2(mb, mb);
-                uint64_t l0 = 0, l1 = 0;                 // (0, 0)
-                if (!my_turn()) return;
-                weights<POLY, 0>(v, tS, scale2, mb2, l0, l1);
-                weights<POLY, 32>(v, tS, scale2, mb2, l0, l1);
-                half_done(0);
-                weights<POLY, 64>(v, tS, scale2, mb2, l0, l1);
-                // (the turn is handed over a little early: the other warp
-                // needs ~190 cycles to see it)
-                arrive_if(lane == 0 && j < turns, &bar->turn[1 - s][quad]);
-                weights<POLY, 96>(v, tS, scale2, mb2, l0, l1);
-                float x, y;
-                unpack2(add2(l0, l1), x, y);
-                sum = x + y;
             }
-            if (m != -INFINITY) l += sum;                // (a row of -inf scores has no weight)
-            half_done(1);
+            __syncwarp();
+            arrive_if(lane == 0, &bar->p_full[s][b]);
         }
         // epilogue: O / l and the log-sum-exp, final or as one of the row's parts
-        if (n > 0) {
+        if (h > 0) {
             if (!tc::mbar_wait(&bar->o_full[s], o_phase, a.err, &bar->abort)) return;
             o_phase ^= 1;
             tc::tc_fence_after();
         }
+        if (h > 1) prev_phase ^= 1;
         if (busy && (w.pair || s == 0 || a.c.max_parts > 1)) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const float out_lse = l == 0.f ? -INFINITY : m * a.s.scale + logf(l);
@@ -819,11 +765,12 @@ full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         tc::mbar_init(&bar->q_full, 1);
         tc::mbar_init(&bar->q_empty, 2);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bar->s_full[i], 1);
-            tc::mbar_init(&bar->p_full[i][0], 4);        // one per softmax warp
-            tc::mbar_init(&bar->p_full[i][1], 4);
+            for (int b = 0; b < 2; ++b) {
+                tc::mbar_init(&bar->s_full[i][b], 1);
+                tc::mbar_init(&bar->p_full[i][b], 4);    // one per softmax warp
+            }
+            tc::mbar_init(&bar->o_prev[i], 1);
             tc::mbar_init(&bar->o_full[i], 1);
-            for (int q = 0; q < 4; ++q) tc::mbar_init(&bar->turn[i][q], 1);
             tc::mbar_init(&bar->item_full[i], 1);
             tc::mbar_init(&bar->item_empty[i], 2 + 1 + 8);   // MMA, check and softmax warps
             bar->odd[i] = 0;
@@ -837,13 +784,11 @@ full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     tc::tc_fence_after();
     const uint32_t tmem = bar->tmem;
     if (warp < 4) {
-        tc::regs_dec<kRegsLoad>();
         if (warp == 0) load_role<D, kPaged>(a, bar, sQ, sKV, &tm_q, &tm_k, &tm_v);
         else if (warp == 3) check_role<D>(a, bar, sKV);
         else if (threadIdx.x % 32 == 0)
             mma_role<D>(a, bar, tmem, tc::smem_u32(sQ), tc::smem_u32(sKV), warp - 1);
     } else {
-        tc::regs_inc<kRegsSoftmax>();
         softmax_role<D, kPaged>(a, bar, tmem, warp / 4 - 1);
     }
     tc::tc_fence_before();
