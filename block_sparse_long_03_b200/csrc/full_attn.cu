@@ -29,6 +29,7 @@ full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *se
     __shared__ int64_t total_tiles;
     __shared__ int32_t base;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    launch_next();
     if (tid < (int)(kErrorBytes / 4)) err[tid] = 0u;
     // offsets: ascending, inside the arrays
     bool bad = false;
@@ -77,9 +78,13 @@ full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *se
             const int n = (int)(((int64_t)seqs[b].L + s.page_size - 1) / s.page_size);
             const int32_t *row = q.block_table + (int64_t)b * s.max_pages;
             bool wrong = false;
-            for (int i = (warp % wps) * 32 + lane; i < n; i += wps * 32) {
-                const int32_t pg = row[i];
-                wrong |= pg < 0 || pg >= s.num_pages;
+            const int step = wps * 32;
+            for (int i0 = (warp % wps) * 32 + lane; i0 < n; i0 += 8 * step) {
+                int32_t pg[8];                     // eight loads in flight
+#pragma unroll
+                for (int u = 0; u < 8; ++u) pg[u] = i0 + u * step < n ? row[i0 + u * step] : 0;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) wrong |= pg[u] < 0 || pg[u] >= s.num_pages;
             }
             if (__any_sync(0xffffffffu, wrong) && lane == 0) {
                 record_error(err, MSA_ERR_BAD_PAGE_TABLE, 3);
@@ -152,48 +157,72 @@ full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *se
 constexpr int kMergeThreads = 256;
 
 // Rows of a token whose keys were split: weights exp(lse_i - max lse), summed
-// in the order of the parts.  One CTA a token, one warp a head at a time,
-// lane l channels 4 l .. 4 l + 3.
+// in the order of the parts.  One warp a (token, head), lane l channels
+// (D / 32) l ...; four parts' loads are in flight at a time (bound: HBM or L2,
+// the partial results once).
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
 full_combine_kernel(FullShape s, FullSeqs q, FullCut c, const FullPlan *plan, const FullSeq *seqs,
                     const float *__restrict__ part_o, const float *__restrict__ part_lse,
                     __nv_bfloat16 *__restrict__ O, float *__restrict__ lse) {
-    if (plan->invalid) return;
-    const int64_t n = blockIdx.x;
+    const int lane = threadIdx.x % 32;
+    const int64_t row = ((int64_t)blockIdx.x * kMergeThreads + threadIdx.x) / 32;
+    const int64_t step = s.tokens * s.Hq;
+    wait_previous();
+    if (row >= step || plan->invalid) return;
+    const int64_t n = row / s.Hq;
+    // the token's sequence: as many sequences end at or before it
     int b = 0;
-    for (int b0 = 0; b0 < s.B; b0 += kMergeThreads)
-        b += __syncthreads_count(b0 + threadIdx.x < s.B && q.cu_q[b0 + threadIdx.x + 1] <= n);
+    for (int b0 = 0; b0 < s.B; b0 += 32) {
+        const unsigned m = __ballot_sync(0xffffffffu, b0 + lane < s.B && q.cu_q[b0 + lane + 1] <= n);
+        b += __popc(m);
+        if (m != 0xffffffffu) break;
+    }
     if (b >= s.B) return;
     const FullSeq sq = seqs[b];
     if (n < sq.q0) return;
     const int parts = full_row_parts(sq, c, (int)(n - sq.q0));
     if (parts == 0) return;
     constexpr int kPer = D / 32;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int h = warp; h < s.Hq; h += kMergeThreads / 32) {
-        const int64_t row = n * s.Hq + h, step = s.tokens * s.Hq;
-        float m = -INFINITY;
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, part_lse[row + i * step]);
-        for (int off = 16; off > 0; off /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        float sum = 0.f, acc[kPer];
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, part_lse[row + i * step]);
+    for (int off = 16; off > 0; off /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float sum = 0.f, acc[kPer];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-        for (int i = 0; i < parts; ++i) {
-            const float l = part_lse[row + i * step];
-            if (l == -INFINITY) continue;          // no key of this part: nothing was stored
-            const float w = expf(l - m);
-            sum += w;
-            const float *src = part_o + (row + i * step) * D + lane * kPer;
+    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += 4) {
+        float l[4], x[4][kPer];
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) acc[k] = fmaf(w, src[k], acc[k]);
+        for (int u = 0; u < 4; ++u) l[u] = i0 + u < parts ? part_lse[row + (i0 + u) * step] : -INFINITY;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            // a part without a key of this row stored nothing
+            const bool use = l[u] != -INFINITY;
+            const float *src = part_o + (row + (i0 + u) * step) * D + lane * kPer;
+            if constexpr (kPer == 4) {
+                const float4 v = use ? *(const float4 *)src : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
+            } else {
+                const float2 v = use ? *(const float2 *)src : make_float2(0.f, 0.f);
+                x[u][0] = v.x; x[u][1] = v.y;
+            }
         }
-        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k)
-            O[row * D + lane * kPer + k] = __float2bfloat16_rn(acc[k] * inv);
-        if (lane == 0) lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
+        for (int u = 0; u < 4; ++u) {
+            const float w = l[u] == -INFINITY ? 0.f : expf(l[u] - m);
+            sum += w;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) acc[k] = fmaf(w, x[u][k], acc[k]);
+        }
     }
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    __nv_bfloat162 o[kPer / 2];
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k)
+        o[k] = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    if constexpr (kPer == 4) *(uint2 *)(O + row * D + lane * kPer) = *(const uint2 *)o;
+    else *(uint32_t *)(O + row * D + lane * kPer) = *(const uint32_t *)o;
+    if (lane == 0) lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
 // ---------------------------------------------------------------- CUDA cores
@@ -402,10 +431,11 @@ cudaError_t launch_full_combine(const FullShape &s, const FullSeqs &q, const Ful
                                 const FullPlan *plan, const FullSeq *seqs, const float *part_o,
                                 const float *part_lse, void *O, float *lse, cudaStream_t st) {
     auto k = s.d == 64 ? full_combine_kernel<64> : full_combine_kernel<128>;
-    k<<<(unsigned)s.tokens, kMergeThreads, 0, st>>>(s, q, c, plan, seqs, part_o, part_lse,
-                                                    (__nv_bfloat16 *)O, lse);
+    const int64_t warps = s.tokens * s.Hq;
     count_launches(1);
-    return cudaGetLastError();
+    return launch_after(k, dim3((unsigned)((warps * 32 + kMergeThreads - 1) / kMergeThreads)),
+                        dim3(kMergeThreads), 0, st, s, q, c, plan, seqs, part_o, part_lse,
+                        (__nv_bfloat16 *)O, lse);
 }
 
 FullCut full_simt_cut(const FullShape &s) { return FullCut{kSimtRows / s.R, 0, 0, 1, 1}; }

@@ -84,6 +84,33 @@ cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut 
                            const void *K, const void *V, void *O, float *lse, float *part_o,
                            float *part_lse, uint32_t *err, cudaStream_t st);
 
+// The call's kernels follow one another closely (programmatic dependent
+// launch): the next one may be set up as soon as every block of this one has
+// called launch_next() or ended, and waits in wait_previous() until this one
+// has ended and its writes are visible; before that it touches no memory that
+// another kernel of the call writes.
+__device__ __forceinline__ void launch_next() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                         A... args) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, static_cast<P>(args)...);
+}
+
 // The sequence that item `i` belongs to, searched from sequence b on (items
 // are visited in ascending order), by one warp.
 __device__ __forceinline__ int full_find_seq(const FullSeq *seqs, int B, int b, int i, int lane) {

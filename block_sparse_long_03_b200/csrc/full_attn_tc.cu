@@ -519,32 +519,6 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     return d;
 }
 
-// 2^x of two values x <= 2^7 on the multiply-add pipe.  With n = round(x) and
-// f = x - n in [-1/2, 1/2]: 2^x = 2^n p(f), p the polynomial of degree 4 with
-// the least largest relative error to 2^f there (found by iteratively
-// reweighted least squares): 2.7e-6, mean 4e-8.  n comes from adding
-// 1.5 * 2^23, whose sum's low bits are n; they are added to p's exponent.
-// x below -126 counts as -126.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t x2) {
-    float x, y;
-    unpack2(x2, x, y);
-    x2 = pack2(fmaxf(x, -126.f), fmaxf(y, -126.f));
-    const float kRound = 12582912.f;
-    const uint64_t r2 = add2(x2, pack2(kRound, kRound));
-    const uint64_t n2 = add2(r2, pack2(-kRound, -kRound));
-    const uint64_t f2 = fma2(n2, pack2(-1.f, -1.f), x2);
-    uint64_t p2 = fma2(f2, pack2(0.009570101276040077f, 0.009570101276040077f),
-                       pack2(0.05591785907745361f, 0.05591785907745361f));
-    p2 = fma2(p2, f2, pack2(0.240247443318367f, 0.240247443318367f));
-    p2 = fma2(p2, f2, pack2(0.6931217908859253f, 0.6931217908859253f));
-    p2 = fma2(p2, f2, pack2(0.9999992847442627f, 0.9999992847442627f));
-    float r, q, p, u;
-    unpack2(r2, r, q);
-    unpack2(p2, p, u);
-    return pack2(__uint_as_float(__float_as_uint(p) + (__float_as_uint(r) << 23)),
-                 __uint_as_float(__float_as_uint(u) + (__float_as_uint(q) << 23)));
-}
-
 // The maximum of a row's 64 scores.
 __device__ __forceinline__ float row_max(const uint32_t (&v)[kHalf]) {
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -556,13 +530,9 @@ __device__ __forceinline__ float row_max(const uint32_t (&v)[kHalf]) {
     return max3_nan(max3_nan(m[0], m[1], m[2]), m[3], m[3]);
 }
 
-#ifndef POLY
-#define POLY 4
-#endif
 // P = 2^(scale_log2 S - mb) of a half, as bf16 over S; returns the fp32 row
-// sum.  Of each 16 pairs kPoly go to the multiply-add pipe, the others to the
-// special-function unit.
-template <int kPoly>
+// sum.  (A quarter of the exponentials as polynomials on the multiply-add pipe
+// gains nothing here: the special-function unit is busy 65 % of the time.)
 __device__ __forceinline__ float weights(const uint32_t (&v)[kHalf], uint32_t tP, uint64_t scale2,
                                          uint64_t mb2) {
     uint64_t l0 = 0, l1 = 0;                             // (0, 0)
@@ -571,19 +541,13 @@ __device__ __forceinline__ float weights(const uint32_t (&v)[kHalf], uint32_t tP
         uint32_t pk[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-            uint64_t x2 = fma2(pack2(__uint_as_float(v[h + 2 * c]), __uint_as_float(v[h + 2 * c + 1])),
-                               scale2, mb2);
+            const uint64_t x2 = fma2(pack2(__uint_as_float(v[h + 2 * c]),
+                                           __uint_as_float(v[h + 2 * c + 1])), scale2, mb2);
             float e0, e1;
-            if ((c + 1) * kPoly / 16 > c * kPoly / 16) {
-                x2 = exp2_poly2(x2);
-                unpack2(x2, e0, e1);
-            } else {
-                unpack2(x2, e0, e1);
-                e0 = tc::ex2_approx(e0);
-                e1 = tc::ex2_approx(e1);
-                x2 = pack2(e0, e1);
-            }
-            if (c & 1) l1 = add2(l1, x2); else l0 = add2(l0, x2);
+            unpack2(x2, e0, e1);
+            e0 = tc::ex2_approx(e0);
+            e1 = tc::ex2_approx(e1);
+            if (c & 1) l1 = add2(l1, pack2(e0, e1)); else l0 = add2(l0, pack2(e0, e1));
             __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
             pk[c] = *(uint32_t *)&b;
         }
@@ -662,9 +626,7 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                     }
                 }
                 const float mb = m == -INFINITY ? 0.f : -m * a.scale_log2;
-                const float sum = edge ? weights<0>(v, tB, scale2, pack2(mb, mb))
-                                       : weights<POLY>(v, tB, scale2, pack2(mb, mb));
-                if (m != -INFINITY) l += sum;            // (a row of -inf scores has no weight)
+                l += weights(v, tB, scale2, pack2(mb, mb));
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
             }
@@ -779,6 +741,8 @@ full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         tc::fence_mbar_init();
     }
     if (warp == 1) tc::tmem_alloc(&bar->tmem, 512);
+    launch_next();
+    wait_previous();                                     // the plan
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -828,9 +792,9 @@ cudaError_t launch_tc_t(const FullShape &s, const TcArgs &a, const void *Q, cons
     if (e != cudaSuccess) return e;
     const int64_t most = (s.tokens / a.c.unit_tokens + std::min<int64_t>(s.B, s.tokens)) * s.Hkv *
                          a.c.max_parts;
-    k<<<(unsigned)std::min<int64_t>(most, sm_count()), kThreads, tc_smem<D>(), st>>>(tq, tk, tv, a);
     count_launches(1);
-    return cudaGetLastError();
+    return launch_after(k, dim3((unsigned)std::min<int64_t>(most, sm_count())), dim3(kThreads),
+                        tc_smem<D>(), st, tq, tk, tv, a);
 }
 
 }  // namespace
