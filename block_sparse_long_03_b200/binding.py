@@ -400,20 +400,25 @@ def _refuse(where: str, why: str):
 
 def _tokens(where, name, t, like=None):
     """The token stride of t [tokens, heads, d], whose heads are dense."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        _refuse(where, f"{name} must be [tokens, heads, d] with dense heads")
-    if t.dtype not in _DTYPE_CODES or (like is not None and (t.dtype != like.dtype or
-                                                             t.device != like.device)):
+    if t.dim() != 3:
+        _refuse(where, f"{name} must be [tokens, heads, d]")
+    (n, heads, d), (step, head, one) = t.shape, t.stride()
+    if (one != 1 and d > 1) or (head != d and heads > 1):
+        _refuse(where, f"{name}: a token's heads must be dense")
+    if like is None:
+        if t.dtype not in _DTYPE_CODES:
+            _refuse(where, f"{name}: dtype {t.dtype}")
+    elif t.dtype is not like.dtype or t.device != like.device:
         _refuse(where, f"{name}: dtype or device")
-    if t.shape[0] <= 1:
+    if n <= 1:
         return 0
-    if t.stride(0) == 0:
+    if step == 0:
         _refuse(where, f"{name}: expanded over tokens")
-    return t.stride(0)
+    return step
 
 
 def _dense(where, name, t, dtype, device, shape):
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         _refuse(where, f"{name} must be dense {dtype} {tuple(shape)} on {device}")
     return t.data_ptr()
 
@@ -422,8 +427,9 @@ def _on_device(where, device, call, *args):
     """call(*args, stream) on the current stream of `device`."""
     if device.type != "cuda":
         _refuse(where, "tensors must be on a CUDA device")
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
+    index = device.index
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
         status = call(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -451,29 +457,36 @@ def _rope_params(where, Q, K, Q_out, K_out, inv_freq, layout, mscale, inverse):
     x = Q if Q is not None else K
     if x is None:
         _refuse(where, "Q and K are both None")
-    if layout not in ROPE_LAYOUTS:
+    code = ROPE_LAYOUTS.get(layout)
+    if code is None:
         _refuse(where, f"layout {layout!r}")
-    p = RopeParams()
-    p.q_stride = p.q_out_stride = p.k_stride = p.k_out_stride = 0
-    p.Hq = p.Hkv = 1
+    q = qo = k = ko = 0
+    Hq = Hkv = 1
     if Q is not None:
-        p.q_stride, p.Hq = _tokens(where, "Q", Q), Q.shape[1]
-        p.q_out_stride = _tokens(where, "Q_out", Q_out, Q)
-        if Q_out.shape != Q.shape:
-            _refuse(where, "Q_out: shape")
+        q, Hq = _tokens(where, "Q", Q), Q.shape[1]
+        if Q_out is not Q:
+            qo = _tokens(where, "Q_out", Q_out, Q)
+            if Q_out.shape != Q.shape:
+                _refuse(where, "Q_out: shape")
+        else:
+            qo = q
     if K is not None:
-        p.k_stride, p.Hkv = _tokens(where, "K", K, x), K.shape[1]
+        k, Hkv = _tokens(where, "K", K, None if Q is None else Q), K.shape[1]
         if K.shape[0] != x.shape[0] or K.shape[2] != x.shape[2]:
             _refuse(where, "K: shape")
-        if K_out is not None:
-            p.k_out_stride = _tokens(where, "K_out", K_out, K)
+        if K_out is K:
+            ko = k
+        elif K_out is not None:
+            ko = _tokens(where, "K_out", K_out, K)
             if K_out.shape != K.shape:
                 _refuse(where, "K_out: shape")
-    _dense(where, "inv_freq", inv_freq, torch.float64, x.device, (inv_freq.numel(),))
-    p.tokens, p.d, p.rot_dim = x.shape[0], x.shape[2], 2 * inv_freq.numel()
-    p.layout, p.inverse, p.dtype = ROPE_LAYOUTS[layout], int(bool(inverse)), _DTYPE_CODES[x.dtype]
-    p.mscale = mscale
-    return p, x
+    half = inv_freq.numel()
+    if (inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or
+            inv_freq.device != x.device or not inv_freq.is_contiguous()):
+        _refuse(where, f"inv_freq must be dense float64 [rot_dim / 2] on {x.device}")
+    n, _, d = x.shape
+    return RopeParams(n, q, k, qo, ko, Hq, Hkv, d, 2 * half, code, int(bool(inverse)),
+                      _DTYPE_CODES[x.dtype], mscale), x
 
 
 def rope(Q, K, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0,
@@ -482,9 +495,9 @@ def rope(Q, K, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0
     positions [tokens] int32, inv_freq [rot_dim / 2] float64.  inverse=True applies the
     transposed map (the gradient).  Q_out=Q, K_out=K turn in place.  Returns (Q_out, K_out)."""
     if Q is not None and Q_out is None:
-        Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        Q_out = Q.new_empty(Q.shape)
     if K is not None and K_out is None:
-        K_out = torch.empty(K.shape, dtype=K.dtype, device=K.device)
+        K_out = K.new_empty(K.shape)
     p, x = _rope_params("rope", Q, K, Q_out, K_out, inv_freq, layout, mscale, inverse)
     pos = _dense("rope", "positions", positions, torch.int32, x.device, (p.tokens,))
     if p.tokens:
@@ -513,7 +526,7 @@ def rope_append_paged(Q, K, V, k_idx, cu_seqlens, seq_lens, block_table, inv_fre
     counts the new tokens.  Returns (Q_out, workspace); the caches are updated in place."""
     where = "rope_append_paged"
     if Q is not None and Q_out is None:
-        Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+        Q_out = Q.new_empty(Q.shape)
     p, x = _rope_params(where, Q, K, Q_out, None, inv_freq, layout, mscale, False)
     B = cu_seqlens.numel() - 1
     _dense(where, "cu_seqlens", cu_seqlens, torch.int32, x.device, (B + 1,))
@@ -546,7 +559,7 @@ def rope_append_paged(Q, K, V, k_idx, cu_seqlens, seq_lens, block_table, inv_fre
 def _attn_call(where, paged, p, Q, out, lse, workspace, call, *args):
     tokens, Hq, d = Q.shape
     if out is None:
-        out = torch.empty((tokens, Hq, d), dtype=Q.dtype, device=Q.device)
+        out = Q.new_empty(Q.shape)
     else:
         _dense(where, "out", out, Q.dtype, Q.device, Q.shape)
     if lse is None:

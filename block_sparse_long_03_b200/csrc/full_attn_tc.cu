@@ -31,6 +31,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "full_attn.cuh"
 #include "tc.cuh"
@@ -763,11 +764,22 @@ full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     }
 }
 
-int sm_count() {
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
+// SMs of the current device, and kernel k's shared-memory limit raised there:
+// looked up and set once per device (together about 2 us a call).
+template <int D, bool kPaged>
+cudaError_t device_ready(int *sms) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    *sms = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
+    if (*sms > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(full_tc_kernel<D, kPaged>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc_smem<D>());
+    if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_release);
+    return e;
 }
 
 template <int D, bool kPaged>
@@ -786,15 +798,14 @@ cudaError_t launch_tc_t(const FullShape &s, const TcArgs &a, const void *Q, cons
     const uint32_t box[3] = {64, 1, (uint32_t)a.box};
     if (!make_tmap_bf16(&tk, s.key_tokens ? K : Q, 3, dims, kstr, box)) return cudaErrorInvalidValue;
     if (!make_tmap_bf16(&tv, s.key_tokens ? V : Q, 3, dims, vstr, box)) return cudaErrorInvalidValue;
-    auto k = full_tc_kernel<D, kPaged>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)tc_smem<D>());
+    int sms = 0;
+    const cudaError_t e = device_ready<D, kPaged>(&sms);
     if (e != cudaSuccess) return e;
     const int64_t most = (s.tokens / a.c.unit_tokens + std::min<int64_t>(s.B, s.tokens)) * s.Hkv *
                          a.c.max_parts;
     count_launches(1);
-    return launch_after(k, dim3((unsigned)std::min<int64_t>(most, sm_count())), dim3(kThreads),
-                        tc_smem<D>(), st, tq, tk, tv, a);
+    return launch_after(full_tc_kernel<D, kPaged>, dim3((unsigned)std::min<int64_t>(most, sms)),
+                        dim3(kThreads), tc_smem<D>(), st, tq, tk, tv, a);
 }
 
 }  // namespace
