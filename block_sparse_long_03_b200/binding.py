@@ -544,9 +544,6 @@ def rope_append_paged(Q, K, V, k_idx, cu_seqlens, seq_lens, block_table, inv_fre
                            (*K_cache.shape[:2], d_idx))
     if workspace is None:
         workspace = torch.empty(256, dtype=torch.uint8, device=x.device)
-    if p.tokens == 0:
-        workspace[:256].zero_()
-        return Q_out, workspace
     _on_device(where, x.device, lib.msa_rope_append_paged, p, B, cu_seqlens.data_ptr(),
                seq_lens.data_ptr(), block_table.data_ptr(), K_cache.shape[1],
                block_table.shape[1], K_cache.shape[0], Q.data_ptr() if Q is not None else None,

@@ -242,11 +242,9 @@ msa_status_t msa_rope_append_paged(
     c.B = B; c.page_size = page_size; c.max_pages = max_pages; c.num_pages = num_pages;
     c.d_idx = k_idx ? d_idx : 0;
     c.err = (uint32_t *)workspace;
-    cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = cudaMemsetAsync(workspace, 0, kErrorBytes, st);
-    if (e == cudaSuccess)
-        e = launch_rope_append(a, c, params->dtype, params->layout == MSA_ROPE_INTERLEAVED, st);
-    return cuda_status(e);
+    return cuda_status(launch_rope_append(a, c, params->dtype,
+                                          params->layout == MSA_ROPE_INTERLEAVED,
+                                          (cudaStream_t)stream));
 }
 
 size_t msa_attn_workspace_size(const msa_attn_params_t *params, int paged) {
