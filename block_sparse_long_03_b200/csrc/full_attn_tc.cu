@@ -812,15 +812,19 @@ cudaError_t launch_tc_t(const FullShape &s, const TcArgs &a, const void *Q, cons
 
 // Two row tiles of 128 / R tokens a unit.  Keys are split into runs while a
 // call has too few units to keep every SM busy several times over: about
-// kItemsPerSm items an SM, runs of at least kMinTiles tiles; the partial
-// results then take at most (items + units) * 256 rows * 2 (about 300 MB).
+// kItemsPerSm items an SM (3, 4, 6, 8: a decode step of 64 sequences 485, 471,
+// 466, 474 us, a mixed step 1112, 1115, 1144, 1160 us).  A run has at least two
+// tiles over a paged cache, where a single token may have 1000 keys and every
+// SM idle (27 us; at least four: 31 us), and four over packed prompts, whose
+// shortest then need no merge (28.7 against 32.8 us).  The partial results
+// take at most (items + units) * 256 rows * 2, about 300 MB.
 FullCut full_tc_cut(const FullShape &s) {
-    constexpr int kItemsPerSm = 6, kMinTiles = 2, kSms = 148;
+    constexpr int kItemsPerSm = 4, kSms = 148;
     FullCut c;
     c.half_tokens = kRows / s.R;
     c.unit_tokens = 2 * c.half_tokens;
     c.split = kSms * kItemsPerSm;
-    c.min_tiles = kMinTiles;
+    c.min_tiles = s.paged ? 2 : 4;
     const int64_t units = std::max<int64_t>(1, (s.tokens + c.unit_tokens - 1) / c.unit_tokens) * s.Hkv;
     c.max_parts = (int)std::min<int64_t>(64, std::max<int64_t>(1, (4 * kSms + units - 1) / units));
     return c;

@@ -80,7 +80,8 @@ msa_status_t make_full(const msa_attn_params_t *p, bool paged, FullShape *s) {
         return MSA_ERR_INVALID_ARG;
     if (p->d != 64 && p->d != 128) return MSA_ERR_UNSUPPORTED;
     if (p->Hq / p->Hkv > 64 || p->Hq > 1024 || p->B > (1 << 20)) return MSA_ERR_UNSUPPORTED;
-    if (p->tokens > 0x7fffffff || (!paged && p->key_tokens > 0x7fffffff)) return MSA_ERR_UNSUPPORTED;
+    if (p->tokens > 0x7fffff00ll || (!paged && p->key_tokens > 0x7fffff00ll))
+        return MSA_ERR_UNSUPPORTED;
     // key positions are 32-bit, cache rows too (they are TMA coordinates)
     if (paged && ((int64_t)p->max_pages * p->page_size > 0x7fffff00ll ||
                   (int64_t)p->num_pages * p->page_size > 0x7fffff00ll))

@@ -404,7 +404,11 @@ MSA_EXPORT msa_status_t msa_decode_paged(const msa_params_t *params, const int32
  * read and their outputs are left as they were.  A sequence may have no
  * tokens.  Strides are in elements, from one token to the next (so that Q, K
  * and V may be slices of one projection's output); 0 means dense; a token's
- * heads are dense.  They must keep every token 16-byte aligned.
+ * heads are dense.  They must keep every token 16-byte aligned.  Offset,
+ * length, position and page arrays are 4-byte aligned, every other pointer as
+ * for the calls above.  The calls may be captured into a graph; the graph then
+ * needs its workspace as long as it lives, and two graphs or calls that may
+ * run at once need a workspace each.
  * --------------------------------------------------------------------- */
 
 /* How a rotated head's channels are paired: channel i with i + rot_dim / 2,
@@ -496,8 +500,9 @@ MSA_EXPORT msa_status_t msa_rope_append_paged(
     void *V_cache, void *k_idx_cache, void *workspace, size_t workspace_bytes, void *stream);
 
 typedef struct {
-    int64_t tokens;      /* rows of Q, O and lse, < 2^31                         */
-    int64_t key_tokens;  /* rows of packed K and V (paged calls: not read)       */
+    int64_t tokens;      /* rows of Q, O and lse, <= 2^31 - 256                  */
+    int64_t key_tokens;  /* rows of packed K and V, <= 2^31 - 256 (paged calls:  */
+                         /* not read)                                            */
     int64_t q_stride, k_stride, v_stride;   /* paged calls read q_stride only    */
     int32_t B;           /* sequences                                            */
     int32_t Hq, Hkv;     /* heads; Hq % Hkv == 0, Hq / Hkv <= 64                 */

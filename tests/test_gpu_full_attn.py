@@ -319,6 +319,79 @@ def test_paged_equals_packed():
         assert bool(((a[1][lo:hi].double() - b[1][lo:hi].double()).abs() <= 2 * lb).all())
 
 
+def test_many_sequences():
+    """1500 sequences of 0 to 4 tokens (more than the plan's threads), packed and paged."""
+    msa, g = _msa(), torch.Generator().manual_seed(71)
+    T = torch.randint(0, 5, (1500,), generator=g).tolist()
+    L = [t + int(x) if t else 0 for t, x in zip(T, torch.randint(0, 40, (1500,), generator=g))]
+    Hq, Hkv, d = 4, 1, 64
+    Ks, Vs, Kc, Vc, table = ref.paginate(L, 8, 1, Hkv, d, BF16, g, "cuda", math.nan)
+    Q = _randn(g, (sum(T), Hq, d), BF16)
+    cu, ck = ref.offsets(T), ref.offsets(L)
+    a = msa.attn_paged(Q.cuda(), Kc, Vc, cu.cuda(), ck.diff().to(torch.int32).cuda(), table)
+    b = msa.attn_packed(Q.cuda(), torch.cat(Ks).cuda(), torch.cat(Vs).cuda(), cu.cuda(), ck.cuda())
+    assert msa.msa_get_device_error(a[2]) == 0 and msa.msa_get_device_error(b[2]) == 0
+    some = [i for i in range(1500) if T[i]][::37]
+    for O, lse, _ in (a, b):
+        for i in some:
+            rows = slice(int(cu[i]), int(cu[i + 1]))
+            ref.assert_attention(O[rows], lse[rows], ref.attention(Q[rows], Ks[i], Vs[i]), f"{i}")
+    assert torch.equal(a[0], b[0])          # one key tile each: the same products in both
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_nothing_to_do_and_no_keys(dtype):
+    """No tokens: the error word is cleared.  Tokens without any key: O = 0, lse = -inf."""
+    msa = _msa()
+    Q = torch.randn((6, 4, 64), device="cuda").to(dtype)
+    none = torch.zeros((0, 2, 64), dtype=dtype, device="cuda")
+    zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    O, _, _ = msa.attn_packed(Q[:0], none, none, zero, workspace=ws)
+    assert O.shape == (0, 4, 64) and msa.msa_get_device_error(ws) == 0
+    cu = torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    O, lse, ws = msa.attn_packed(Q, none, none, cu, zero)
+    assert msa.msa_get_device_error(ws) == 0
+    assert bool((O == 0).all()) and bool((lse == -math.inf).all())
+
+
+def test_output_16_byte_aligned():
+    """O 16 but not 32 bytes aligned: the same bits."""
+    msa, g = _msa(), torch.Generator().manual_seed(81)
+    n, H, d = 300, 2, 64
+    Q, K, V = (_randn(g, (n, H, d), BF16).cuda() for _ in range(3))
+    cu = ref.offsets([n]).cuda()
+    want = msa.attn_packed(Q, K, V, cu)
+    room = torch.zeros(n * H * d + 16, dtype=BF16, device="cuda")
+    at = 8 if room.data_ptr() % 32 == 0 else 0
+    out = room[at:at + n * H * d].view(n, H, d)
+    assert out.data_ptr() % 32 == 16
+    msa.attn_packed(Q, K, V, cu, out=out)
+    assert torch.equal(out, want[0])
+
+
+def test_two_calls_at_once():
+    """Calls on two streams that may overlap, a workspace each, give the bits of calls alone."""
+    msa, g = _msa(), torch.Generator().manual_seed(91)
+    jobs = []
+    for T, L in (([64] * 4, [3000, 2000, 900, 64]), ([1] * 40, [1500] * 40)):
+        _, _, Kc, Vc, table = ref.paginate(L, 64, 1, 4, 128, BF16, g, "cuda", math.nan)
+        Q = _randn(g, (sum(T), 16, 128), BF16).cuda()
+        jobs.append((Q, Kc, Vc, ref.offsets(T).cuda(), torch.tensor(L, dtype=torch.int32).cuda(),
+                     table))
+    alone = [msa.attn_paged(*j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        got = []
+        for j, st in zip(jobs, streams):
+            with torch.cuda.stream(st):
+                got.append(msa.attn_paged(*j))
+        torch.cuda.synchronize()
+        for x, y in zip(got, alone):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
 # ---------------------------------------------------------------- together
 
 def test_serving_run():

@@ -98,7 +98,7 @@ BAD_ATTN = [
     (dict(tokens=-1), 1), (dict(B=0), 1), (dict(Hq=0), 1), (dict(Hq=7), 1), (dict(d=0), 1),
     (dict(dtype=3), 1), (dict(scale=math.nan), 1), (dict(scale=math.inf), 1), (dict(d=96), 2),
     (dict(Hq=130), 2), (dict(Hq=2048, Hkv=512), 2), (dict(B=1 << 21), 2), (dict(tokens=1 << 31), 2),
-    (dict(q_stride=1000), 1), (dict(q_stride=1028), 1),
+    (dict(q_stride=1000), 1), (dict(q_stride=1028), 1), (dict(tokens=(1 << 31) - 255), 2),
 ]
 
 
