@@ -453,7 +453,23 @@ def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: str = "non
     return out.to(device or "cuda")
 
 
+def _like(x):
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _out_stride(where, name, out, x, x_stride):
+    """The token stride of an output the caller gave for x."""
+    if out is x:
+        return x_stride
+    stride = _tokens(where, name, out, x)
+    if out.shape != x.shape:
+        _refuse(where, f"{name}: shape")
+    return stride
+
+
 def _rope_params(where, Q, K, Q_out, K_out, inv_freq, layout, mscale, inverse):
+    """The parameters of a call (an output of None: a dense one) and the tensor whose tokens,
+    type and device they are."""
     x = Q if Q is not None else K
     if x is None:
         _refuse(where, "Q and K are both None")
@@ -462,31 +478,23 @@ def _rope_params(where, Q, K, Q_out, K_out, inv_freq, layout, mscale, inverse):
         _refuse(where, f"layout {layout!r}")
     q = qo = k = ko = 0
     Hq = Hkv = 1
+    n, _, d = x.shape if x.dim() == 3 else (0, 0, 0)
     if Q is not None:
         q, Hq = _tokens(where, "Q", Q), Q.shape[1]
-        if Q_out is not Q:
-            qo = _tokens(where, "Q_out", Q_out, Q)
-            if Q_out.shape != Q.shape:
-                _refuse(where, "Q_out: shape")
-        else:
-            qo = q
+        if Q_out is not None:
+            qo = _out_stride(where, "Q_out", Q_out, Q, q)
     if K is not None:
-        k, Hkv = _tokens(where, "K", K, None if Q is None else Q), K.shape[1]
-        if K.shape[0] != x.shape[0] or K.shape[2] != x.shape[2]:
+        k = _tokens(where, "K", K, Q)
+        kn, Hkv, kd = K.shape
+        if kn != n or kd != d:
             _refuse(where, "K: shape")
-        if K_out is K:
-            ko = k
-        elif K_out is not None:
-            ko = _tokens(where, "K_out", K_out, K)
-            if K_out.shape != K.shape:
-                _refuse(where, "K_out: shape")
-    half = inv_freq.numel()
+        if K_out is not None:
+            ko = _out_stride(where, "K_out", K_out, K, k)
     if (inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or
-            inv_freq.device != x.device or not inv_freq.is_contiguous()):
+            not inv_freq.is_contiguous() or inv_freq.device != x.device):
         _refuse(where, f"inv_freq must be dense float64 [rot_dim / 2] on {x.device}")
-    n, _, d = x.shape
-    return RopeParams(n, q, k, qo, ko, Hq, Hkv, d, 2 * half, code, int(bool(inverse)),
-                      _DTYPE_CODES[x.dtype], mscale), x
+    return RopeParams(n, q, k, qo, ko, Hq, Hkv, d, 2 * inv_freq.numel(), code,
+                      1 if inverse else 0, _DTYPE_CODES[x.dtype], mscale), x
 
 
 def rope(Q, K, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0,
@@ -494,12 +502,12 @@ def rope(Q, K, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0
     """Rotary positions on Q [tokens, Hq, d] and K [tokens, Hkv, d] (either may be None);
     positions [tokens] int32, inv_freq [rot_dim / 2] float64.  inverse=True applies the
     transposed map (the gradient).  Q_out=Q, K_out=K turn in place.  Returns (Q_out, K_out)."""
-    if Q is not None and Q_out is None:
-        Q_out = Q.new_empty(Q.shape)
-    if K is not None and K_out is None:
-        K_out = K.new_empty(K.shape)
     p, x = _rope_params("rope", Q, K, Q_out, K_out, inv_freq, layout, mscale, inverse)
     pos = _dense("rope", "positions", positions, torch.int32, x.device, (p.tokens,))
+    if Q is not None and Q_out is None:
+        Q_out = _like(Q)
+    if K is not None and K_out is None:
+        K_out = _like(K)
     if p.tokens:
         _on_device("rope", x.device, lib.msa_rope, p, Q.data_ptr() if Q is not None else None,
                    K.data_ptr() if K is not None else None, pos, inv_freq.data_ptr(),
@@ -525,9 +533,9 @@ def rope_append_paged(Q, K, V, k_idx, cu_seqlens, seq_lens, block_table, inv_fre
     V are packed [tokens, heads, d] (Q may be None), k_idx [tokens, d_idx] or None; seq_lens
     counts the new tokens.  Returns (Q_out, workspace); the caches are updated in place."""
     where = "rope_append_paged"
-    if Q is not None and Q_out is None:
-        Q_out = Q.new_empty(Q.shape)
     p, x = _rope_params(where, Q, K, Q_out, None, inv_freq, layout, mscale, False)
+    if Q is not None and Q_out is None:
+        Q_out = _like(Q)
     B = cu_seqlens.numel() - 1
     _dense(where, "cu_seqlens", cu_seqlens, torch.int32, x.device, (B + 1,))
     _paged_args(where, B, K_cache, V_cache, seq_lens, block_table, x.dtype, x.device)
@@ -554,9 +562,10 @@ def rope_append_paged(Q, K, V, k_idx, cu_seqlens, seq_lens, block_table, inv_fre
 
 
 def _attn_call(where, paged, p, Q, out, lse, workspace, call, *args):
+    p.q_stride = _tokens(where, "Q", Q)
     tokens, Hq, d = Q.shape
     if out is None:
-        out = Q.new_empty(Q.shape)
+        out = _like(Q)
     else:
         _dense(where, "out", out, Q.dtype, Q.device, Q.shape)
     if lse is None:
@@ -564,7 +573,6 @@ def _attn_call(where, paged, p, Q, out, lse, workspace, call, *args):
     else:
         _dense(where, "lse", lse, torch.float32, Q.device, (tokens, Hq))
     p.tokens, p.Hq, p.d, p.dtype = tokens, Hq, d, _DTYPE_CODES[Q.dtype]
-    p.q_stride = _tokens(where, "Q", Q)
     if workspace is None:
         n = lib.msa_attn_workspace_size(p, paged)
         if n == 0:

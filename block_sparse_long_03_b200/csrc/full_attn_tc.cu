@@ -187,8 +187,8 @@ __device__ __forceinline__ bool for_tiles(const Item &w, FK k, FV v) {
 
 template <int D, bool kPaged>
 __device__ void load_role(const TcArgs &a, Bars *bar, uint8_t *sQ, uint8_t *sKV,
-                          const CUtensorMap *tm_q, const CUtensorMap *tm_k,
-                          const CUtensorMap *tm_v) {
+                          const CUtensorMap *tm_q, const CUtensorMap *tm_q1,
+                          const CUtensorMap *tm_k, const CUtensorMap *tm_v) {
     constexpr int kAtoms = D / 64, kSlots = ring_slots<D>();
     constexpr uint32_t kTile = 128 * D * 2;
     const int lane = threadIdx.x % 32;
@@ -219,9 +219,20 @@ __device__ void load_role(const TcArgs &a, Bars *bar, uint8_t *sQ, uint8_t *sKV,
             if (!tc::mbar_wait(&bar->q_empty, (q_uses & 1) ^ 1, a.err, &bar->abort)) break;
             ++q_uses;
             const int tiles = w.pair ? 2 : 1;
-            if (lane == 0) tc::mbar_expect_tx(&bar->q_full, q_tile_bytes * tiles);
+            const bool one = w.nt == 1;
+            if (lane == 0)
+                tc::mbar_expect_tx(&bar->q_full, one ? (uint32_t)a.s.R * 128 * kAtoms
+                                                     : q_tile_bytes * tiles);
             __syncwarp();
-            if (lane < tiles * kAtoms) {
+            if (one) {
+                // one token: its heads alone.  The other rows then stay 0 in a
+                // decode step, and the products on them cost little power,
+                // which bounds the clock (1000 W at 1.7 GHz with the rows of
+                // other sequences there).
+                if (lane < kAtoms)
+                    tc::tma_load_3d(sQ + lane * 16384, tm_q1, &bar->q_full, lane * 64,
+                                    w.g * a.s.R, w.q0);
+            } else if (lane < tiles * kAtoms) {
                 const int t = lane / kAtoms, at = lane % kAtoms;
                 tc::tma_load_3d(sQ + t * kTile + at * 16384, tm_q, &bar->q_full, at * 64,
                                 w.g * a.s.R, w.q0 + t * a.c.half_tokens);
@@ -709,8 +720,9 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
 
 template <int D, bool kPaged>
 __global__ void __launch_bounds__(kThreads, 1)
-full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcArgs a) {
+full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
+               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+               const __grid_constant__ TcArgs a) {
     constexpr int kSlots = ring_slots<D>();
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -742,6 +754,10 @@ full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         tc::fence_mbar_init();
     }
     if (warp == 1) tc::tmem_alloc(&bar->tmem, 512);
+    // rows of Q that are never loaded are 0
+    for (int i = threadIdx.x; i < 2 * 128 * D * 2 / 16; i += kThreads)
+        ((uint4 *)sQ)[i] = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     launch_next();
     wait_previous();                                     // the plan
     tc::tc_fence_before();
@@ -749,7 +765,7 @@ full_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     tc::tc_fence_after();
     const uint32_t tmem = bar->tmem;
     if (warp < 4) {
-        if (warp == 0) load_role<D, kPaged>(a, bar, sQ, sKV, &tm_q, &tm_k, &tm_v);
+        if (warp == 0) load_role<D, kPaged>(a, bar, sQ, sKV, &tm_q, &tm_q1, &tm_k, &tm_v);
         else if (warp == 3) check_role<D>(a, bar, sKV);
         else if (threadIdx.x % 32 == 0)
             mma_role<D>(a, bar, tmem, tc::smem_u32(sQ), tc::smem_u32(sKV), warp - 1);
@@ -785,11 +801,13 @@ cudaError_t device_ready(int *sms) {
 template <int D, bool kPaged>
 cudaError_t launch_tc_t(const FullShape &s, const TcArgs &a, const void *Q, const void *K,
                         const void *V, cudaStream_t st) {
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tq1, tk, tv;
     const uint64_t qdims[3] = {(uint64_t)D, (uint64_t)s.Hq, (uint64_t)s.tokens};
     const uint64_t qstr[2] = {(uint64_t)D * 2, (uint64_t)s.q_stride * 2};
     const uint32_t qbox[3] = {64, (uint32_t)s.R, (uint32_t)a.c.half_tokens};
+    const uint32_t qbox1[3] = {64, (uint32_t)s.R, 1};
     if (!make_tmap_bf16(&tq, Q, 3, qdims, qstr, qbox)) return cudaErrorInvalidValue;
+    if (!make_tmap_bf16(&tq1, Q, 3, qdims, qstr, qbox1)) return cudaErrorInvalidValue;
     // no keys at all: nothing is loaded, but a map needs an extent
     const uint64_t rows = (uint64_t)std::max<int64_t>(s.key_tokens, 1);
     const uint64_t dims[3] = {(uint64_t)D, (uint64_t)s.Hkv, rows};
@@ -805,7 +823,7 @@ cudaError_t launch_tc_t(const FullShape &s, const TcArgs &a, const void *Q, cons
                          a.c.max_parts;
     count_launches(1);
     return launch_after(full_tc_kernel<D, kPaged>, dim3((unsigned)std::min<int64_t>(most, sms)),
-                        dim3(kThreads), tc_smem<D>(), st, tq, tk, tv, a);
+                        dim3(kThreads), tc_smem<D>(), st, tq, tq1, tk, tv, a);
 }
 
 }  // namespace
