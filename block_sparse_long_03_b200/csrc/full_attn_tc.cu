@@ -23,11 +23,21 @@
 // hand-overs, 1400 of 3800 cycles a tile, while neither the tensor cores nor
 // the special-function units were half busy.
 //
-// The running maximum m a row's P is taken against moves only when a tile's
-// maximum passes it by more than 2^8: P stays below 2^8 (the same relative
-// rounding in bf16, far from fp32's range) and O is rarely rescaled.  The
-// fp32 row sum is of the unrounded P.  TMEM: S/P of the streams in columns
-// 0 and 128, O in 256 and 384.
+// The running maximum m that a row's P is taken against moves only when a
+// half's maximum would make P larger than 2^8: P keeps the same relative
+// rounding in bf16, far from fp32's range, and O is rarely rescaled.  The fp32
+// row sum is of the unrounded P.
+//
+// Measured (one B200 at its 1000 W limit, 1.65 to 1.8 GHz): one 32768-token
+// prompt of 32 heads, d = 128, 8.0 to 8.4 ms, 1.05 to 1.10 PFLOP/s on the
+// causal flops, 64 to 67 % of a measured 8192^3 matrix product; tensor pipe 53 %
+// busy, special-function units 53 %.  The products alone (no softmax) take
+// 6.2 to 6.8 ms of that, the softmax alone 5.9 to 6.5.  A decode step of 64
+// sequences of 2K to 16K keys: 440 us, 5.9 TB/s, 90 % of a copy.
+// Tried and slower: S released as soon as the softmax has it in registers, P
+// in columns of its own (8.5 ms); four softmax warpgroups, two a stream taking
+// halves in turn (8.9 ms); a quarter to a half of the exponentials as
+// polynomials on the multiply-add pipe (no gain).
 #include <math.h>
 
 #include <algorithm>
