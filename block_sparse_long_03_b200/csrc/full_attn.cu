@@ -22,15 +22,61 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
+constexpr int kRowPages = 256;           // pages a warp looks at in one go
+constexpr int kLongRows = 1024;
+
+__device__ __forceinline__ int pages_of(int32_t L, int page_size) {
+    return (int)(((uint32_t)L + (uint32_t)page_size - 1u) / (uint32_t)page_size);
+}
+
+// Marks the sequences b0 .. b0 + kSeqs - 1 that have a bad page id (k0 = -1; L
+// is still being read).  A warp's lanes take 32 pages of each at a time, eight
+// loads in flight.  Rows of more than `limit` pages are left out.
+template <int kSeqs>
+__device__ __forceinline__ void check_rows(const FullShape &s, const int32_t *table, FullSeq *seqs,
+                                           int b0, int limit, int lane, uint32_t *err) {
+    int n[kSeqs], most = 0;
+#pragma unroll
+    for (int j = 0; j < kSeqs; ++j) {
+        n[j] = b0 + j < s.B ? pages_of(seqs[b0 + j].L, s.page_size) : 0;
+        if (n[j] > limit) n[j] = 0;
+        most = max(most, n[j]);
+    }
+    const int32_t *row = table + (int64_t)b0 * s.max_pages + lane;
+    unsigned wrong = 0;
+    for (int i0 = 0; i0 < most; i0 += 8 / kSeqs * 32) {
+        int32_t pg[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u / kSeqs * 32;
+            pg[u] = i + lane < n[u % kSeqs] ? row[(int64_t)(u % kSeqs) * s.max_pages + i] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (pg[u] < 0 || pg[u] >= s.num_pages) wrong |= 1u << u % kSeqs;
+    }
+    wrong = __reduce_or_sync(0xffffffffu, wrong);
+    if (lane < kSeqs && (wrong >> lane & 1)) {
+        record_error(err, MSA_ERR_BAD_PAGE_TABLE, 3);
+        seqs[b0 + lane].k0 = -1;
+    }
+}
+
+// One CTA: checks what the device arrays say, sizes the key runs and numbers
+// the items.  Latency is all it costs, so loads go out in batches: a warp
+// takes one to eight short rows of the block table at a time, and the long
+// ones are cut over all warps.
 __global__ void __launch_bounds__(kPlanThreads)
 full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *seqs,
                  uint32_t *err) {
     __shared__ int64_t warp_sum[32];
     __shared__ int64_t total_tiles;
-    __shared__ int32_t base;
+    __shared__ int32_t base, n_long;
+    __shared__ int2 long_rows[kLongRows];          // sequence, pages
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     launch_next();
     if (tid < (int)(kErrorBytes / 4)) err[tid] = 0u;
+    if (tid == 0) n_long = 0;
     // offsets: ascending, inside the arrays
     bool bad = false;
     for (int b = tid; b < s.B; b += kPlanThreads) {
@@ -61,6 +107,11 @@ full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *se
                 L = 0;
                 record_error(err, MSA_ERR_BAD_PAGE_TABLE, 3);
             }
+            const int n = pages_of(L, s.page_size);
+            if (n > kRowPages) {
+                const int i = atomicAdd(&n_long, 1);
+                if (i < kLongRows) long_rows[i] = make_int2(b, n);
+            }
         } else {
             k0 = q.cu_k[b];
             L = q.cu_k[b + 1] - k0;
@@ -72,24 +123,38 @@ full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *se
     }
     __syncthreads();
     if (s.paged) {
-        // wps warps a sequence (more than one where there are few sequences)
-        const int wps = max(1, 32 / s.B), at_once = 32 / wps;
-        for (int b = warp / wps; b < s.B && warp < at_once * wps; b += at_once) {
-            const int n = (int)(((int64_t)seqs[b].L + s.page_size - 1) / s.page_size);
-            const int32_t *row = q.block_table + (int64_t)b * s.max_pages;
+        const bool listed = n_long <= kLongRows;
+        const int limit = listed ? kRowPages : 0x7fffffff;
+        if (s.B > 128)
+            for (int b = warp * 8; b < s.B; b += 256)
+                check_rows<8>(s, q.block_table, seqs, b, limit, lane, err);
+        else if (s.B > 64) {
+            if (warp * 4 < s.B) check_rows<4>(s, q.block_table, seqs, warp * 4, limit, lane, err);
+        } else if (s.B > 32) {
+            if (warp * 2 < s.B) check_rows<2>(s, q.block_table, seqs, warp * 2, limit, lane, err);
+        } else if (warp < s.B)
+            check_rows<1>(s, q.block_table, seqs, warp, limit, lane, err);
+        int turn = 0;                              // the warp whose turn it is
+        for (int e = 0; listed && e < n_long; ++e) {
+            const int2 r = long_rows[e];
+            const int32_t *row = q.block_table + (int64_t)r.x * s.max_pages;
+            const int pieces = (r.y + kRowPages - 1) / kRowPages;
             bool wrong = false;
-            const int step = wps * 32;
-            for (int i0 = (warp % wps) * 32 + lane; i0 < n; i0 += 8 * step) {
-                int32_t pg[8];                     // eight loads in flight
+            for (int p = (warp - turn) & 31; p < pieces; p += 32) {
+                int32_t pg[8];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) pg[u] = i0 + u * step < n ? row[i0 + u * step] : 0;
+                for (int u = 0; u < 8; ++u) {
+                    const int i = p * kRowPages + u * 32 + lane;
+                    pg[u] = i < r.y ? row[i] : 0;
+                }
 #pragma unroll
                 for (int u = 0; u < 8; ++u) wrong |= pg[u] < 0 || pg[u] >= s.num_pages;
             }
             if (__any_sync(0xffffffffu, wrong) && lane == 0) {
                 record_error(err, MSA_ERR_BAD_PAGE_TABLE, 3);
-                seqs[b].k0 = -1;                   // marked; L is still being read
+                seqs[r.x].k0 = -1;
             }
+            turn = (turn + pieces) & 31;
         }
         __syncthreads();
         for (int b = tid; b < s.B; b += kPlanThreads)
@@ -156,11 +221,41 @@ full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *se
 
 constexpr int kMergeThreads = 256;
 
+// Adds parts i0 .. i0 + N - 1 (in that order) to a row: lane i % 32 of mine
+// holds part i's lse.  All N loads are in flight at once.
+template <int N, int kPer>
+__device__ __forceinline__ void add_parts(int i0, int parts, float mine, float m, const float *src,
+                                          int64_t part_step, float &sum, float (&acc)[kPer]) {
+    float l[N], x[N][kPer];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        l[u] = __shfl_sync(0xffffffffu, mine, (i0 + u) % 32);
+        if (i0 + u >= parts) l[u] = -INFINITY;
+        // a part without a key of this row stored nothing
+        const bool use = l[u] != -INFINITY;
+        const float *p = src + (i0 + u) * part_step;
+        if constexpr (kPer == 4) {
+            const float4 v = use ? *(const float4 *)p : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
+        } else {
+            const float2 v = use ? *(const float2 *)p : make_float2(0.f, 0.f);
+            x[u][0] = v.x; x[u][1] = v.y;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const float w = l[u] == -INFINITY ? 0.f : expf(l[u] - m);
+        sum += w;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] = fmaf(w, x[u][k], acc[k]);
+    }
+}
+
 // Rows of a token whose keys were split: weights exp(lse_i - max lse), summed
 // in the order of the parts.  One warp a (token, head), lane l channels
-// (D / 32) l ...; four parts' loads are in flight at a time (bound: HBM or L2,
-// the partial results once).
-template <int D>
+// (D / 32) l ...; N parts' loads are in flight at a time (bound: HBM or L2,
+// the partial results once; for few rows of many parts the loads' latency).
+template <int D, int N>
 __global__ void __launch_bounds__(kMergeThreads)
 full_combine_kernel(FullShape s, FullSeqs q, FullCut c, const FullPlan *plan, const FullSeq *seqs,
                     const float *__restrict__ part_o, const float *__restrict__ part_lse,
@@ -171,12 +266,15 @@ full_combine_kernel(FullShape s, FullSeqs q, FullCut c, const FullPlan *plan, co
     wait_previous();
     if (row >= step || plan->invalid) return;
     const int64_t n = row / s.Hq;
-    // the token's sequence: as many sequences end at or before it
+    // the token's sequence: as many sequences end at or before it; 32 marks a
+    // step, of which the last one passed leaves a 32nd of the range
     int b = 0;
-    for (int b0 = 0; b0 < s.B; b0 += 32) {
-        const unsigned m = __ballot_sync(0xffffffffu, b0 + lane < s.B && q.cu_q[b0 + lane + 1] <= n);
-        b += __popc(m);
-        if (m != 0xffffffffu) break;
+    for (int len = s.B; len > 0;) {
+        const int stride = (len + 31) / 32, e = (lane + 1) * stride;
+        const unsigned m = __ballot_sync(0xffffffffu, e <= len && q.cu_q[b + e] <= n);
+        const int passed = __popc(m) * stride;
+        b += passed;
+        len = min(stride - 1, len - passed);
     }
     if (b >= s.B) return;
     const FullSeq sq = seqs[b];
@@ -184,36 +282,22 @@ full_combine_kernel(FullShape s, FullSeqs q, FullCut c, const FullPlan *plan, co
     const int parts = full_row_parts(sq, c, (int)(n - sq.q0));
     if (parts == 0) return;
     constexpr int kPer = D / 32;
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, part_lse[row + i * step]);
+    // lane l holds the lse of part l, and in turn those of parts l + 32 ...
+    // (loops, so that the code of a cold call stays small)
+    const float *row_lse = part_lse + row;
+    float mine = lane < parts ? row_lse[lane * step] : -INFINITY, m = mine;
+#pragma unroll 1
+    for (int i = 32 + lane; i < parts; i += 32) m = fmaxf(m, row_lse[i * step]);
     for (int off = 16; off > 0; off /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     float sum = 0.f, acc[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += 4) {
-        float l[4], x[4][kPer];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) l[u] = i0 + u < parts ? part_lse[row + (i0 + u) * step] : -INFINITY;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            // a part without a key of this row stored nothing
-            const bool use = l[u] != -INFINITY;
-            const float *src = part_o + (row + (i0 + u) * step) * D + lane * kPer;
-            if constexpr (kPer == 4) {
-                const float4 v = use ? *(const float4 *)src : make_float4(0.f, 0.f, 0.f, 0.f);
-                x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
-            } else {
-                const float2 v = use ? *(const float2 *)src : make_float2(0.f, 0.f);
-                x[u][0] = v.x; x[u][1] = v.y;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float w = l[u] == -INFINITY ? 0.f : expf(l[u] - m);
-            sum += w;
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) acc[k] = fmaf(w, x[u][k], acc[k]);
-        }
+    const float *src = part_o + row * D + lane * kPer;
+#pragma unroll 1
+    for (int i0 = 0; i0 < parts; i0 += N) {
+        if (i0 > 0 && i0 % 32 == 0)
+            mine = i0 + lane < parts ? row_lse[(i0 + lane) * step] : -INFINITY;
+        add_parts<N>(i0, parts, mine, m, src, step * D, sum, acc);
     }
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     __nv_bfloat162 o[kPer / 2];
@@ -236,11 +320,11 @@ constexpr int kSimtKeys = 32;
 // x + 24; softmax: two threads a row; values: rows 4 y .. and channels
 // 4 x + 32 k ...  A score costs d multiply-adds from shared memory and so
 // does a weight: 64 of them for each eight 16-byte reads.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads)
 full_simt_kernel(FullShape s, FullSeqs sq, FullCut c, const FullPlan *plan, const FullSeq *seqs,
-                 const T *__restrict__ Q, const T *__restrict__ K, const T *__restrict__ V,
-                 T *__restrict__ O, float *__restrict__ lse) {
+                 const float *__restrict__ Q, const float *__restrict__ K,
+                 const float *__restrict__ V, float *__restrict__ O, float *__restrict__ lse) {
     constexpr int kLd = D + 4;
     extern __shared__ __align__(16) float sm[];
     float *qs = sm;                                        // [64][D + 4]
@@ -266,9 +350,9 @@ full_simt_kernel(FullShape s, FullSeqs sq, FullCut c, const FullPlan *plan, cons
             const int r = i / (D / 4), ch = (i % (D / 4)) * 4;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
-                const T *p = Q + (int64_t)(q.q0 + t0 + r / s.R) * s.q_stride +
+                const float *p = Q + (int64_t)(q.q0 + t0 + r / s.R) * s.q_stride +
                              (int64_t)(g * s.R + r % s.R) * D + ch;
-                v = make_float4(to_f32(p[0]), to_f32(p[1]), to_f32(p[2]), to_f32(p[3]));
+                v = *(const float4 *)p;
             }
             *(float4 *)(qs + r * kLd + ch) = v;
         }
@@ -293,10 +377,10 @@ full_simt_kernel(FullShape s, FullSeqs sq, FullCut c, const FullPlan *plan, cons
                         in = MSA_IN_BOUNDS(kr, (int64_t)s.num_pages * s.page_size);
                     }
                     if (in) {
-                        const T *kp = K + kr * s.k_stride + (int64_t)g * D + ch;
-                        const T *vp = V + kr * s.v_stride + (int64_t)g * D + ch;
-                        kv = make_float4(to_f32(kp[0]), to_f32(kp[1]), to_f32(kp[2]), to_f32(kp[3]));
-                        vv = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
+                        const float *kp = K + kr * s.k_stride + (int64_t)g * D + ch;
+                        const float *vp = V + kr * s.v_stride + (int64_t)g * D + ch;
+                        kv = *(const float4 *)kp;
+                        vv = *(const float4 *)vp;
                     }
                 }
                 *(float4 *)(ks + r * kLd + ch) = kv;
@@ -390,30 +474,30 @@ full_simt_kernel(FullShape s, FullSeqs sq, FullCut c, const FullPlan *plan, cons
         for (int i = 0; i < 4; ++i) {
             const int r = 4 * y + i;
             if (r >= rows) continue;
-            T *dst = O + ((int64_t)(q.q0 + t0 + r / s.R) * s.Hq + g * s.R + r % s.R) * D;
+            float *dst = O + ((int64_t)(q.q0 + t0 + r / s.R) * s.Hq + g * s.R + r % s.R) * D;
             const float inv = inv_l[r];
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    dst[4 * x + 32 * k + e] = from_f32<T>(acc[i][4 * k + e] * inv);
+                *(float4 *)(dst + 4 * x + 32 * k) =
+                    make_float4(acc[i][4 * k] * inv, acc[i][4 * k + 1] * inv,
+                                acc[i][4 * k + 2] * inv, acc[i][4 * k + 3] * inv);
         }
         __syncthreads();
     }
 }
 
-template <typename T, int D>
-cudaError_t launch_simt_t(const FullShape &s, const FullSeqs &q, const FullCut &c,
+template <int D>
+cudaError_t launch_simt(const FullShape &s, const FullSeqs &q, const FullCut &c,
                           const FullPlan *plan, const FullSeq *seqs, const void *Q, const void *K,
                           const void *V, void *O, float *lse, cudaStream_t st) {
     const size_t smem = sizeof(float) * ((size_t)(kSimtRows + kSimtKeys) * (D + 4) + kSimtKeys * D +
                                          kSimtRows * 36 + 2 * kSimtRows);
-    auto k = full_simt_kernel<T, D>;
+    auto k = full_simt_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t most = (s.tokens / c.unit_tokens + s.B) * s.Hkv;
     k<<<(unsigned)std::min<int64_t>(most, 148 * 3 * 16), kSimtThreads, smem, st>>>(
-        s, q, c, plan, seqs, (const T *)Q, (const T *)K, (const T *)V, (T *)O, lse);
+        s, q, c, plan, seqs, (const float *)Q, (const float *)K, (const float *)V, (float *)O, lse);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -430,8 +514,14 @@ cudaError_t launch_full_plan(const FullShape &s, const FullSeqs &q, const FullCu
 cudaError_t launch_full_combine(const FullShape &s, const FullSeqs &q, const FullCut &c,
                                 const FullPlan *plan, const FullSeq *seqs, const float *part_o,
                                 const float *part_lse, void *O, float *lse, cudaStream_t st) {
-    auto k = s.d == 64 ? full_combine_kernel<64> : full_combine_kernel<128>;
+    // Up to 16 warps an SM, all resident at sixteen loads a lane in flight
+    // (64 rows of 128 parts among 2048: 20 us; four loads: 33); beyond, four, which
+    // leave room for 48 warps (a 2048-token step of 65 sequences: 415 us in
+    // all; sixteen loads: 460).
     const int64_t warps = s.tokens * s.Hq;
+    const bool few = warps <= 148 * 16;
+    auto k = s.d == 64 ? (few ? full_combine_kernel<64, 16> : full_combine_kernel<64, 4>)
+                       : (few ? full_combine_kernel<128, 16> : full_combine_kernel<128, 4>);
     count_launches(1);
     return launch_after(k, dim3((unsigned)((warps * 32 + kMergeThreads - 1) / kMergeThreads)),
                         dim3(kMergeThreads), 0, st, s, q, c, plan, seqs, part_o, part_lse,
@@ -443,12 +533,8 @@ FullCut full_simt_cut(const FullShape &s) { return FullCut{kSimtRows / s.R, 0, 0
 cudaError_t launch_full_simt(const FullShape &s, const FullSeqs &q, const FullCut &c,
                              const FullPlan *plan, const FullSeq *seqs, const void *Q,
                              const void *K, const void *V, void *O, float *lse, cudaStream_t st) {
-    if (s.dtype == MSA_BF16)
-        return s.d == 64
-                   ? launch_simt_t<__nv_bfloat16, 64>(s, q, c, plan, seqs, Q, K, V, O, lse, st)
-                   : launch_simt_t<__nv_bfloat16, 128>(s, q, c, plan, seqs, Q, K, V, O, lse, st);
-    return s.d == 64 ? launch_simt_t<float, 64>(s, q, c, plan, seqs, Q, K, V, O, lse, st)
-                     : launch_simt_t<float, 128>(s, q, c, plan, seqs, Q, K, V, O, lse, st);
+    return s.d == 64 ? launch_simt<64>(s, q, c, plan, seqs, Q, K, V, O, lse, st)
+                     : launch_simt<128>(s, q, c, plan, seqs, Q, K, V, O, lse, st);
 }
 
 }  // namespace msa

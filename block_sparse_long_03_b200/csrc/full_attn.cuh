@@ -44,6 +44,8 @@ struct FullPlan {
 constexpr size_t kPlanBytes = 256;
 
 constexpr int kFullKeys = 128;           // keys of a tile
+constexpr int kMaxParts = 64;            // key runs of a unit, at most (twice as many partial
+                                         // results where two row tiles share a run)
 
 // How a kernel's tiles cut the work: unit_tokens queries a unit; with
 // split > 0 the key runs are sized for about `split` items in all, at most

@@ -854,7 +854,7 @@ FullCut full_tc_cut(const FullShape &s) {
     c.split = kSms * kItemsPerSm;
     c.min_tiles = s.paged ? 2 : 4;
     const int64_t units = std::max<int64_t>(1, (s.tokens + c.unit_tokens - 1) / c.unit_tokens) * s.Hkv;
-    c.max_parts = (int)std::min<int64_t>(64, std::max<int64_t>(1, (4 * kSms + units - 1) / units));
+    c.max_parts = (int)std::min<int64_t>(kMaxParts, std::max<int64_t>(1, (4 * kSms + units - 1) / units));
     return c;
 }
 

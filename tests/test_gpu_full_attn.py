@@ -258,6 +258,56 @@ def test_paged_bad_sequences_are_skipped(dtype):
     assert bool((O == 0).all()) and msa.msa_get_device_error(ws) == 7
 
 
+@pytest.mark.parametrize("B,long_pages", [(31, 0), (100, 300), (300, 900), (1300, 0)])
+def test_paged_bad_pages_among_many(B, long_pages):
+    """Bad page ids at the first, a middle and the last page of short and long rows of batches
+    of every size: those sequences give O = 0 and lse = -inf, the others as usual."""
+    msa, g = _msa(), torch.Generator().manual_seed(B)
+    page, Hkv, Hq, d = 8, 1, 2, 64
+    max_pages = max(long_pages, 40)
+    L = torch.randint(1, 40 * page + 1, (B,), generator=g)
+    if long_pages:
+        L[::7] = torch.randint(257 * page, long_pages * page + 1, (len(L[::7]),), generator=g)
+    n_pages = -(-L // page)
+    Kc, Vc = (_randn(g, (max_pages, page, Hkv, d), BF16).cuda() for _ in range(2))
+    table = torch.randint(0, max_pages, (B, max_pages), generator=g, dtype=torch.int32)
+    bad = torch.rand(B, generator=g) < 0.2
+    for b in torch.nonzero(bad)[:, 0].tolist():
+        at = (0, int(n_pages[b]) // 2, int(n_pages[b]) - 1)[b % 3]
+        table[b, at] = -1 if b % 2 else max_pages
+    for b in range(B):
+        table[b, int(n_pages[b]):] = -(1 << 30)
+    Q = _randn(g, (B, Hq, d), BF16)
+    O, lse, ws = msa.attn_paged(Q.cuda(), Kc, Vc, ref.offsets([1] * B).cuda(), L.int().cuda(),
+                                table.cuda())
+    assert msa.msa_get_device_error(ws) == 7
+    assert bool((O[bad.cuda()] == 0).all()) and bool((lse[bad.cuda()] == -math.inf).all())
+    for b in torch.nonzero(~bad)[:, 0].tolist():
+        rows = table[b, :int(n_pages[b])].long().cuda()
+        K, V = (x[rows].reshape(-1, Hkv, d)[:int(L[b])] for x in (Kc, Vc))
+        ref.assert_attention(O[b:b + 1], lse[b:b + 1],
+                             ref.attention(Q[b:b + 1].cuda(), K, V), f"sequence {b}")
+
+
+def test_paged_rows_outside_with_split_keys():
+    """Rows before the first and behind the last sequence stay as they were where the results
+    come in parts; queries as a slice of a fused projection."""
+    msa, g = _msa(), torch.Generator().manual_seed(37)
+    T, L, page, Hq, Hkv, d, lead, tail = [1, 0, 5], [3000, 70, 4500], 16, 8, 2, 128, 3, 4
+    Ks, Vs, Kc, Vc, table = ref.paginate(L, page, 2, Hkv, d, BF16, g, "cuda", math.nan)
+    n = lead + sum(T) + tail
+    fused = _randn(g, (n, Hq + 4, d), BF16).cuda()
+    cu = ref.offsets(T, lead)
+    out = torch.full((n, Hq, d), 7.0, dtype=BF16, device="cuda")
+    lse = torch.full((n, Hq), 7.0, device="cuda")
+    _, _, ws = msa.attn_paged(fused[:, :Hq], Kc, Vc, cu.cuda(),
+                              torch.tensor(L, dtype=torch.int32).cuda(), table, out=out, lse=lse)
+    assert msa.msa_get_device_error(ws) == 0
+    _check(out, lse, fused[:, :Hq], Ks, Vs, cu)
+    for x in (out, lse):
+        assert bool((x[:lead] == 7).all()) and bool((x[n - tail:] == 7).all())
+
+
 @pytest.mark.parametrize("cu", [[0, 5, 3, 9], [-1, 2, 3, 9], [0, 2, 3, 10]])
 def test_bad_offsets_write_nothing(cu):
     msa = _msa()
