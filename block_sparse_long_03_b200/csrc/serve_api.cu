@@ -220,12 +220,23 @@ msa_status_t msa_rope_append_paged(
     const void *k_idx, int32_t d_idx, const double *inv_freq, void *Q_out, void *K_cache,
     void *V_cache, void *k_idx_cache, void *workspace, size_t workspace_bytes, void *stream) {
     RopeArgs a;
+    const bool none = params != nullptr && params->tokens == 0;   // tokens' pointers may be NULL
+    msa_rope_params_t dense;
+    if (none) {
+        dense = *params;
+        dense.q_stride = dense.q_out_stride = dense.k_stride = v_stride = 0;
+        params = &dense;
+        Q = Q_out = nullptr;
+        if (K == nullptr) K = K_cache;
+        if (V == nullptr) V = V_cache;
+    }
     const msa_status_t rc = make_rope(params, Q, Q_out, K, K_cache, inv_freq, true, &a);
     if (rc != MSA_OK) return rc;
     if (params->inverse != 0 || B <= 0 || page_size <= 0 || max_pages <= 0 || num_pages <= 0)
         return MSA_ERR_INVALID_ARG;
     if (!cu_seqlens || !seq_lens || !block_table || !K || !V || !V_cache) return MSA_ERR_INVALID_ARG;
-    if ((k_idx == nullptr) != (k_idx_cache == nullptr)) return MSA_ERR_INVALID_ARG;
+    if ((k_idx == nullptr) != (k_idx_cache == nullptr) && !(none && k_idx == nullptr))
+        return MSA_ERR_INVALID_ARG;
     if (k_idx != nullptr && d_idx <= 0) return MSA_ERR_INVALID_ARG;
     if (!aligned16(V) || !aligned16(V_cache) || !aligned16(k_idx) || !aligned16(k_idx_cache) ||
         ((uintptr_t)cu_seqlens & 3u) || ((uintptr_t)seq_lens & 3u) || ((uintptr_t)block_table & 3u))

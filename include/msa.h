@@ -483,6 +483,8 @@ MSA_EXPORT msa_status_t msa_rope(const msa_rope_params_t *params, const void *Q,
  * V [tokens, Hkv, d] with v_stride; k_idx [tokens, d_idx] dense, written as
  * it is (turn it with msa_rope first where the model does), d_idx a multiple
  * of 16, <= 128, or k_idx = k_idx_cache = NULL.  Q = Q_out = NULL: keys only.
+ * tokens may be 0 (Q, Q_out, K, V and k_idx may be NULL then): the call only
+ * checks the offsets.
  * seq_lens, block_table, page_size, max_pages, num_pages and the caches: as
  * msa_decode_paged.  Two tokens must not have the same cache row.
  * workspace: at least 256 bytes, 256-byte aligned: the device error word.

@@ -202,6 +202,31 @@ def test_append_without_queries_and_bad_sequences():
     assert msa.msa_get_device_error(ws) == 0        # the next call starts clean
 
 
+@pytest.mark.parametrize("with_idx", [False, True])
+def test_append_of_no_tokens(with_idx):
+    """A step in which no sequence has a new token: nothing is written, the error word is
+    cleared, and offsets past the (empty) tokens are still found."""
+    msa, g = _msa(), _gen(17)
+    Kc, Vc = (torch.randn((3, 16, 2, 64), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    Ic = torch.randn((3, 16, 32), generator=g).to(torch.bfloat16).cuda() if with_idx else None
+    caches = [x.clone() for x in (Kc, Vc, Ic) if x is not None]
+    Q, K, V = (torch.empty((0, h, 64), dtype=torch.bfloat16, device="cuda") for h in (4, 2, 2))
+    x = torch.empty((0, 32), dtype=torch.bfloat16, device="cuda") if with_idx else None
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([5, 0], dtype=torch.int32, device="cuda")
+    table = torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+    ws = torch.full((256,), 9, dtype=torch.uint8, device="cuda")
+    f = msa.rope_frequencies(64)
+    for q in (Q, None):
+        out, _ = msa.rope_append_paged(q, K, V, x, cu, lens, table, f, Kc, Vc, Ic, workspace=ws)
+        assert (out is None) == (q is None) and msa.msa_get_device_error(ws) == 0
+    cu[2] = 1
+    msa.rope_append_paged(Q, K, V, x, cu, lens, table, f, Kc, Vc, Ic, workspace=ws)
+    assert msa.msa_get_device_error(ws) == 7
+    for got, old in zip((x for x in (Kc, Vc, Ic) if x is not None), caches):
+        assert torch.equal(got, old)
+
+
 def test_rope_on_another_stream_and_in_a_graph():
     msa, g = _msa(), _gen(13)
     Q = torch.randn((50, 4, 128), generator=g).to(torch.bfloat16).cuda()
