@@ -423,6 +423,12 @@ def _dense(where, name, t, dtype, device, shape):
     return t.data_ptr()
 
 
+def _workspace(where, ws, device):
+    """A caller's workspace: memory of another device would be a bad address to the kernels."""
+    if ws.device != device or not ws.is_contiguous():
+        _refuse(where, f"workspace must be dense on {device}")
+
+
 def _on_device(where, device, call, *args):
     """call(*args, stream) on the current stream of `device`."""
     if device.type != "cuda":
@@ -501,7 +507,8 @@ def rope(Q, K, positions, inv_freq, *, layout: str = "half", mscale: float = 1.0
          inverse: bool = False, Q_out=None, K_out=None):
     """Rotary positions on Q [tokens, Hq, d] and K [tokens, Hkv, d] (either may be None);
     positions [tokens] int32, inv_freq [rot_dim / 2] float64.  inverse=True applies the
-    transposed map (the gradient).  Q_out=Q, K_out=K turn in place.  Returns (Q_out, K_out)."""
+    transposed map (the gradient; like every call here this one records nothing for autograd).
+    Q_out=Q, K_out=K turn in place.  Returns (Q_out, K_out)."""
     p, x = _rope_params("rope", Q, K, Q_out, K_out, inv_freq, layout, mscale, inverse)
     pos = _dense("rope", "positions", positions, torch.int32, x.device, (p.tokens,))
     if Q is not None and Q_out is None:
@@ -533,6 +540,8 @@ def rope_append_paged(Q, K, V, k_idx, cu_seqlens, seq_lens, block_table, inv_fre
     V are packed [tokens, heads, d] (Q may be None), k_idx [tokens, d_idx] or None; seq_lens
     counts the new tokens.  Returns (Q_out, workspace); the caches are updated in place."""
     where = "rope_append_paged"
+    if K is None or V is None:
+        _refuse(where, "K and V are needed")
     p, x = _rope_params(where, Q, K, Q_out, None, inv_freq, layout, mscale, False)
     if Q is not None and Q_out is None:
         Q_out = _like(Q)
@@ -552,6 +561,8 @@ def rope_append_paged(Q, K, V, k_idx, cu_seqlens, seq_lens, block_table, inv_fre
                            (*K_cache.shape[:2], d_idx))
     if workspace is None:
         workspace = torch.empty(256, dtype=torch.uint8, device=x.device)
+    else:
+        _workspace(where, workspace, x.device)
     _on_device(where, x.device, lib.msa_rope_append_paged, p, B, cu_seqlens.data_ptr(),
                seq_lens.data_ptr(), block_table.data_ptr(), K_cache.shape[1],
                block_table.shape[1], K_cache.shape[0], Q.data_ptr() if Q is not None else None,
@@ -578,6 +589,8 @@ def _attn_call(where, paged, p, Q, out, lse, workspace, call, *args):
         if n == 0:
             raise MsaError(2, f"{where}: sizes not supported")
         workspace = torch.empty(n, dtype=torch.uint8, device=Q.device)
+    else:
+        _workspace(where, workspace, Q.device)
     _on_device(where, Q.device, call, p, Q.data_ptr(), *args, out.data_ptr(), lse.data_ptr(),
                workspace.data_ptr(), workspace.numel())
     return out, lse, workspace

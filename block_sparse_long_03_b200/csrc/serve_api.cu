@@ -149,6 +149,8 @@ msa_status_t run_full(const msa_attn_params_t *params, bool paged, const void *Q
     const FullLayout L = full_layout(s, c);
     if (!workspace || ((uintptr_t)workspace % kAlign) != 0 || workspace_bytes < L.total)
         return MSA_ERR_WORKSPACE;
+    // a row may be written while another row's inputs are still read
+    if (s.tokens > 0 && (O == Q || O == K || O == V || O == lse)) return MSA_ERR_INVALID_ARG;
     char *ws = (char *)workspace;
     uint32_t *err = (uint32_t *)ws;
     FullPlan *plan = (FullPlan *)(ws + L.plan);

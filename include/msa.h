@@ -532,7 +532,7 @@ MSA_EXPORT size_t msa_attn_workspace_size(const msa_attn_params_t *params, int p
  * Q [tokens, Hq, d], K, V [key_tokens, Hkv, d] (dtype, read); cu_seqlens_q,
  * cu_seqlens_k [B + 1] int32 (device, read; the same array for plain
  * prompts); O [tokens, Hq, d] dense (dtype, written), lse [tokens, Hq]
- * float32 (written).  workspace: msa_attn_workspace_size(params, 0) bytes,
+ * float32 (written); neither may overlap an input.  workspace: msa_attn_workspace_size(params, 0) bytes,
  * 256-byte aligned, used by one call at a time; first 256 bytes: the device
  * error word.
  *

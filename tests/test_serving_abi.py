@@ -221,3 +221,31 @@ def test_python_refusals():
         with pytest.raises(b.MsaError):
             call()
             raise AssertionError(f"call {i} was not refused")
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_attention_output_over_an_input(paged):
+    p = _attn()
+    for name in ("Q", "K", "V", "lse"):
+        kw = {"Q": 0x30000, "K": 0x40000, "V": 0x50000, "lse": 0x60000, "O": 0x70000}
+        kw[name] = kw["O"]
+        assert _call_attn(p, paged, **kw) == 1, name
+
+
+def test_python_refuses_foreign_workspaces_and_missing_keys():
+    """A workspace of another device or with gaps, and a cache write without K or V."""
+    b = _lib()
+    for ws in (torch.zeros(4096, dtype=torch.uint8), torch.zeros(4096, dtype=torch.uint8,
+                                                                 device="meta")[::2]):
+        with pytest.raises(b.MsaError) as e:
+            b._workspace("call", ws, torch.device("meta"))
+        assert e.value.status == 1
+    b._workspace("call", torch.zeros(4096, dtype=torch.uint8, device="meta"),
+                 torch.device("meta"))
+    k = torch.zeros((4, 1, 64), dtype=torch.bfloat16)
+    cache = torch.zeros((2, 16, 1, 64), dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    f = torch.ones(32, dtype=torch.float64)
+    for K, V in ((None, k), (k, None)):
+        with pytest.raises(b.MsaError):
+            b.rope_append_paged(k, K, V, None, i, i[:1], i.view(1, 2), f, cache, cache)
