@@ -219,6 +219,21 @@ __device__ void load_role(const TcArgs &a, Bars *bar, uint8_t *sQ, uint8_t *sKV,
             b = full_find_seq(a.seqs, a.s.B, b, item, lane);
             w = make_item(a, a.seqs[b], b, item);
         }
+        const int limit = w.pos0 + w.nt;                 // no row attends key `limit` or later
+        // paged: this lane's box, the cache row of each stream's tile, and of
+        // its next one (whose page id is on its way meanwhile)
+        int row[2] = {0, 0}, next_pg[2] = {0, 0}, next_at[2] = {0, 0};
+        auto look_up = [&](int s, int j) {
+            const int first = (stream_a(w, s) + j) * kFullKeys + lane * a.box;
+            if (lane * a.box >= kFullKeys || first >= limit) return;
+            const int i = first / a.s.page_size, at = first - i * a.s.page_size;
+            const int pg = __ldg(a.q.block_table + (int64_t)w.b * a.s.max_pages + i);
+            if (s) { next_pg[1] = pg; next_at[1] = at; } else { next_pg[0] = pg; next_at[0] = at; }
+        };
+        if (kPaged && w.h0 + w.h1 > 0) {
+            look_up(0, 0);
+            if (!shared_keys(w)) look_up(1, 0);
+        }
         if (!tc::mbar_wait(&bar->item_empty[slot], ((k >> 1) & 1) ^ 1, a.err, &bar->abort)) break;
         if (lane == 0) {
             bar->item[slot] = w;
@@ -248,8 +263,6 @@ __device__ void load_role(const TcArgs &a, Bars *bar, uint8_t *sQ, uint8_t *sKV,
                                 w.g * a.s.R, w.q0 + t * a.c.half_tokens);
             }
         }
-        const int limit = w.pos0 + w.nt;                 // no row attends key `limit` or later
-        int row[2] = {0, 0};                             // paged: this lane's box of the tile
         auto load = [&](const CUtensorMap *tm, int s, int j, bool is_key) {
             if (!tc::mbar_wait(&bar->empty[ring.slot], ring.phase ^ 1, a.err, &bar->abort))
                 return false;
@@ -264,11 +277,9 @@ __device__ void load_role(const TcArgs &a, Bars *bar, uint8_t *sQ, uint8_t *sKV,
             } else {
                 const int first = key + lane * a.box;    // this lane's box
                 const bool mine = lane * a.box < kFullKeys && first < limit;
-                if (is_key && mine) {
-                    const int pg = __ldg(a.q.block_table + (int64_t)w.b * a.s.max_pages +
-                                         first / a.s.page_size);
-                    const int rw = pg * a.s.page_size + first % a.s.page_size;
-                    if (s) row[1] = rw; else row[0] = rw;
+                if (is_key) {
+                    if (s) row[1] = next_pg[1] * a.s.page_size + next_at[1];
+                    else row[0] = next_pg[0] * a.s.page_size + next_at[0];
                 }
                 const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
                 if (lane == 0) tc::mbar_expect_tx(full, (uint32_t)boxes * a.box * 128 * kAtoms);
@@ -280,6 +291,7 @@ __device__ void load_role(const TcArgs &a, Bars *bar, uint8_t *sQ, uint8_t *sKV,
                         tc::tma_load_3d(dst + at * 16384 + lane * a.box * 128, tm, full, at * 64,
                                         w.g, rw);
                 }
+                if (is_key) look_up(s, j + 1);
             }
             if (!is_key && lane == 0 && edge_tile(w, stream_a(w, s) + j))
                 tc::mbar_arrive(&bar->issued[ring.slot]);
