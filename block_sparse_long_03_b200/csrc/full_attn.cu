@@ -266,16 +266,7 @@ full_combine_kernel(FullShape s, FullSeqs q, FullCut c, const FullPlan *plan, co
     wait_previous();
     if (row >= step || plan->invalid) return;
     const int64_t n = row / s.Hq;
-    // the token's sequence: as many sequences end at or before it; 32 marks a
-    // step, of which the last one passed leaves a 32nd of the range
-    int b = 0;
-    for (int len = s.B; len > 0;) {
-        const int stride = (len + 31) / 32, e = (lane + 1) * stride;
-        const unsigned m = __ballot_sync(0xffffffffu, e <= len && q.cu_q[b + e] <= n);
-        const int passed = __popc(m) * stride;
-        b += passed;
-        len = min(stride - 1, len - passed);
-    }
+    const int b = seq_of_token(q.cu_q, s.B, n);
     if (b >= s.B) return;
     const FullSeq sq = seqs[b];
     if (n < sq.q0) return;

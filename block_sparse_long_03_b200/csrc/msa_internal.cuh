@@ -148,6 +148,21 @@ cudaError_t launch_slot_csr(const Shape &s, const int32_t *ids, int tpt, int64_t
 size_t slot_csr_records(const Shape &s, int64_t rc, int tpt);
 int slot_csr_record_ints(int tpt);
 
+// The sequence of packed token n, by one warp: as many sequences end at or
+// before it.  32 marks a step; the last one passed leaves a 32nd of the range.
+__device__ __forceinline__ int seq_of_token(const int32_t *cu, int B, int64_t n) {
+    const int lane = threadIdx.x % 32;
+    int b = 0;
+    for (int len = B; len > 0;) {
+        const int stride = (len + 31) / 32, e = (lane + 1) * stride;
+        const unsigned m = __ballot_sync(0xffffffffu, e <= len && cu[b + e] <= n);
+        const int passed = __popc(m) * stride;
+        b += passed;
+        len = min(stride - 1, len - passed);
+    }
+    return b;
+}
+
 // The indexer's KL target of query rows [r0, r0 + rc) from their partial
 // LSEs and merged lse (run after their merge).
 cudaError_t launch_block_mass(const Shape &s, const int32_t *ids, const float *part_lse,

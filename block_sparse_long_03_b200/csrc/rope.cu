@@ -226,18 +226,6 @@ rope_kernel(RopeArgs a, int shares) {
     k.run(l, a, (T *)a.K_out + n * a.ko_stride, a.Hkv, shares, mine);
 }
 
-// The sequence of token n: as many sequences end at or before it (one warp).
-__device__ __forceinline__ int find_sequence(const int32_t *cu, int B, int64_t n) {
-    const int lane = threadIdx.x % 32;
-    int b = 0;
-    for (int b0 = 0; b0 < B; b0 += 32) {
-        const unsigned m = __ballot_sync(0xffffffffu, b0 + lane < B && cu[b0 + lane + 1] <= n);
-        b += __popc(m);
-        if (m != 0xffffffffu) break;
-    }
-    return b;
-}
-
 // Sequence b's offsets and length are usable: T = hi - lo new tokens, the last
 // of L positions.
 __device__ __forceinline__ bool usable(const RopeArgs &a, const AppendArgs &c, int64_t lo,
@@ -247,28 +235,52 @@ __device__ __forceinline__ bool usable(const RopeArgs &a, const AppendArgs &c, i
 }
 
 // The error word of the call, by one CTA of its own (so that no separate clear
-// is needed): what the other CTAs skip is found again here.
+// is needed): what the other CTAs skip is found again here.  A thread takes a
+// sequence, and warps together those with new tokens on more than four pages
+// (the call for 300 single tokens: 5.5 us; with a warp a sequence 33).
 __device__ __forceinline__ void append_check(const RopeArgs &a, const AppendArgs &c) {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    __shared__ int4 many[kThreads];                // sequence, first and last page
+    __shared__ int n_many;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    auto bad_page = [&](int b, int64_t i) {
+        const int pg = c.block_table[(int64_t)b * c.max_pages + i];
+        return pg < 0 || pg >= c.num_pages;
+    };
     int bad = 0;
-    for (int b = warp; b < c.B; b += kThreads / 32) {
-        const int64_t lo = c.cu_seqlens[b], hi = c.cu_seqlens[b + 1], L = c.seq_lens[b];
-        if (lo == hi) continue;
-        if (!usable(a, c, lo, hi, L)) {
-            ++bad;
-            continue;
+    for (int b0 = 0; b0 < c.B; b0 += kThreads) {
+        if (tid == 0) n_many = 0;
+        __syncthreads();
+        const int b = b0 + tid;
+        if (b < c.B) {
+            const int64_t lo = c.cu_seqlens[b], hi = c.cu_seqlens[b + 1], L = c.seq_lens[b];
+            if (lo != hi && !usable(a, c, lo, hi, L)) {
+                ++bad;
+            } else if (lo != hi) {
+                const int first = (int)((L - (hi - lo)) / c.page_size), last = (int)((L - 1) / c.page_size);
+                if (last - first >= 4) {
+                    many[atomicAdd(&n_many, 1)] = make_int4(b, first, last, 0);
+                } else {
+                    bool wrong = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) wrong |= first + i <= last && bad_page(b, first + i);
+                    bad += wrong;
+                }
+            }
         }
-        bool wrong = false;
-        for (int64_t i = (L - (hi - lo)) / c.page_size + lane; i <= (L - 1) / c.page_size; i += 32) {
-            const int pg = c.block_table[(int64_t)b * c.max_pages + i];
-            wrong |= pg < 0 || pg >= c.num_pages;
+        __syncthreads();
+        for (int e = warp; e < n_many; e += kThreads / 32) {
+            const int4 r = many[e];
+            bool wrong = false;
+            for (int i = r.y + lane; i <= r.z; i += 32) wrong |= bad_page(r.x, i);
+            wrong = __any_sync(0xffffffffu, wrong);
+            bad += lane == 0 && wrong;
         }
-        bad += __any_sync(0xffffffffu, wrong);
+        __syncthreads();
     }
     __shared__ int total;
-    if (threadIdx.x == 0) total = 0;
+    if (tid == 0) total = 0;
     __syncthreads();
-    if (lane == 0 && bad) atomicAdd(&total, bad);
+    if (bad) atomicAdd(&total, bad);
     __syncthreads();
     if (threadIdx.x < kErrorBytes / 4)
         c.err[threadIdx.x] = threadIdx.x == 0 ? (total ? MSA_ERR_BAD_PAGE_TABLE : MSA_OK)
@@ -307,7 +319,7 @@ rope_append_kernel(RopeArgs a, AppendArgs c, int shares) {
     Heads<T, kSide> q, k;
     q.begin(l, a, (const T *)a.Q + n * a.q_stride, a.Hq, share, shares);
     // the token's sequence, position and cache row
-    const int b = find_sequence(c.cu_seqlens, c.B, n);
+    const int b = seq_of_token(c.cu_seqlens, c.B, n);
     if (b >= c.B) return;                                   // behind the last sequence
     const int64_t lo = c.cu_seqlens[b], hi = c.cu_seqlens[b + 1], L = c.seq_lens[b];
     if (n < lo || n >= hi || !usable(a, c, lo, hi, L)) return;

@@ -202,6 +202,55 @@ def test_append_without_queries_and_bad_sequences():
     assert msa.msa_get_device_error(ws) == 0        # the next call starts clean
 
 
+@pytest.mark.parametrize("B", [33, 257, 1100])
+def test_append_of_many_sequences(B):
+    """Single tokens, none, and runs over one to ten pages of many sequences; some have a bad page
+    among those of their new tokens (its tokens are skipped), some behind or before them."""
+    msa, g = _msa(), _gen(B)
+    page, Hkv, d = 16, 1, 16
+    T = torch.randint(0, 3, (B,), generator=g)
+    T[::5] = torch.randint(1, 150, (len(T[::5]),), generator=g)
+    L = T + torch.randint(0, 40, (B,), generator=g)
+    n_pages = -(-L // page)
+    max_pages, total = int(n_pages.max()) + 1, int(n_pages.sum())
+    order = torch.randperm(total, generator=g, dtype=torch.int32)
+    table = torch.full((B, max_pages), -5, dtype=torch.int32)
+    at = 0
+    for b in range(B):
+        k = int(n_pages[b])
+        table[b, :k] = order[at:at + k]
+        at += k
+        if b % 7 == 3 and k:
+            table[b, b % k] = total + B if b % 2 else -1
+    cu = ref.offsets(T.tolist())
+    K, V = (torch.randn((int(cu[-1]), Hkv, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    cache = torch.zeros((total + B, page, Hkv, d), dtype=torch.bfloat16)
+    want, skipped = cache.flatten(0, 1).clone(), 0
+    for b in range(B):
+        for t in range(int(T[b])):
+            p = int(L[b] - T[b]) + t
+            pg = int(table[b, p // page])
+            if 0 <= pg < total + B:
+                want[pg * page + p % page] = V[int(cu[b]) + t]
+            else:
+                skipped += 1
+    assert skipped
+    kc, vc = cache.cuda(), cache.cuda()
+    args = (None, K.cuda(), V.cuda(), None, cu.cuda(), L.int().cuda())
+    f = msa.rope_frequencies(16)
+    _, ws = msa.rope_append_paged(*args, table.cuda(), f, kc, vc)
+    assert msa.msa_get_device_error(ws) == 7
+    assert torch.equal(vc.flatten(0, 1).cpu(), want)
+    for b in range(B):                                # without new tokens behind them: no error
+        if b % 7 == 3:
+            lo, hi = int(L[b] - T[b]) // page, int(n_pages[b])
+            row = table[b, lo:hi]
+            row[(row < 0) | (row >= total)] = total + b
+    kc.zero_(), vc.zero_()
+    _, ws = msa.rope_append_paged(*args, table.cuda(), f, kc, vc)
+    assert msa.msa_get_device_error(ws) == 0
+
+
 @pytest.mark.parametrize("with_idx", [False, True])
 def test_append_of_no_tokens(with_idx):
     """A step in which no sequence has a new token: nothing is written, the error word is
