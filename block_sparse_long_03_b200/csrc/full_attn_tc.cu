@@ -853,7 +853,8 @@ cudaError_t launch_tc_t(const FullShape &s, const TcArgs &a, const void *Q, cons
 // Two row tiles of 128 / R tokens a unit.  Keys are split into runs while a
 // call has too few units to keep every SM busy several times over: about
 // kItemsPerSm items an SM (3, 4, 6, 8: a decode step of 64 sequences 485, 471,
-// 466, 474 us, a mixed step 1112, 1115, 1144, 1160 us).  A run has at least two
+// 466, 474 us, a mixed step 1112, 1115, 1144, 1160 us; with page ids looked up
+// ahead, at four, 463 and 1075).  A run has at least two
 // tiles over a paged cache, where a single token may have 1000 keys and every
 // SM idle (27 us; at least four: 31 us), and four over packed prompts, whose
 // shortest then need no merge (28.7 against 32.8 us).  The partial results
