@@ -67,7 +67,7 @@ struct TcArgs {
     const FullPlan *plan;
     const FullSeq *seqs;
     int *next;                           // the next item to take
-    const __nv_bfloat16 *V;
+    const __nv_bfloat16 *Q, *K, *V;      // Q, K: read for infinite values' weights only
     __nv_bfloat16 *O;
     float *lse, *part_o, *part_lse;
     uint32_t *err;
@@ -445,7 +445,8 @@ __device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ,
 // keys the row does not attend, and 0 times infinity or NaN would reach it:
 // rows of V that no row attends (other sequences, what a page held before)
 // are set to 0, and in rows that only later tokens attend, infinities and
-// NaN are (the epilogue adds them for the rows that do attend them).
+// NaN are (the epilogue adds them, times their weights, for the rows that do
+// attend them).
 template <int D>
 __device__ void check_role(const TcArgs &a, Bars *bar, uint8_t *sKV) {
     constexpr int kSlots = ring_slots<D>(), kChunks = D / 8;
@@ -592,6 +593,17 @@ __device__ __forceinline__ float weights(const uint32_t (&v)[kHalf], uint32_t tP
     return x + y;
 }
 
+// The weight of key row k in query row q, against the running maximum m: for
+// an infinity or NaN among the values, which the products left out.  A weight
+// of 0 (a score of -infinity, or far below m) then gives NaN, as in a product.
+template <int D>
+__device__ __noinline__ float weight_of(const __nv_bfloat16 *q, const __nv_bfloat16 *k,
+                                        float scale_log2, float m) {
+    float dot = 0.f;
+    for (int c = 0; c < D; ++c) dot = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), dot);
+    return tc::ex2_approx(fmaf(dot, scale_log2, m == -INFINITY ? 0.f : -m * scale_log2));
+}
+
 template <int D, bool kPaged>
 __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
     const int quad = (threadIdx.x / 32) % 4, lane = threadIdx.x % 32;
@@ -698,7 +710,7 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         x[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
-                    if (odd && valid) {
+                    if (odd && valid && l != 0.f) {
                         const int hi = min(first_pos + tok, (t0 + n) * kFullKeys - 1);
                         for (int jk = max(t0 * kFullKeys, w.pos0 + 1); jk <= hi; ++jk) {
                             int64_t kr = (int64_t)w.k0 + jk;
@@ -707,10 +719,17 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                                                               jk / a.s.page_size] * a.s.page_size +
                                      jk % a.s.page_size;
                             const __nv_bfloat16 *vp = a.V + kr * a.s.v_stride + (int64_t)w.g * D + c;
+                            bool any = false;
+                            for (int i = 0; i < 32; ++i) any |= !isfinite(__bfloat162float(vp[i]));
+                            if (!any) continue;
+                            const float p = weight_of<D>(
+                                a.Q + (int64_t)(w.q0 + first_tok + tok) * a.s.q_stride +
+                                    (int64_t)(w.g * a.s.R + head) * D,
+                                a.K + kr * a.s.k_stride + (int64_t)w.g * D, a.scale_log2, m);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 const float f = __bfloat162float(vp[i]);
-                                if (!isfinite(f)) x[i] += f;
+                                if (!isfinite(f)) x[i] = fmaf(p, f, x[i]);
                             }
                         }
                     }
@@ -879,6 +898,8 @@ cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut 
     a.s = s; a.q = q; a.c = c;
     a.plan = plan; a.seqs = seqs;
     a.next = (int *)&plan->next;
+    a.Q = (const __nv_bfloat16 *)Q;
+    a.K = (const __nv_bfloat16 *)K;
     a.V = (const __nv_bfloat16 *)V;
     a.O = (__nv_bfloat16 *)O;
     a.lse = lse; a.part_o = part_o; a.part_lse = part_lse; a.err = err;

@@ -526,8 +526,11 @@ MSA_EXPORT size_t msa_attn_workspace_size(const msa_attn_params_t *params, int p
  *   lse[t, h]  = log(sum_j exp(s_j))
  * over the sequence's own keys.  A query with no key (p(t) < 0) gets O = 0
  * and lse = -infinity.  Keys and values that a query does not attend have no
- * influence on it, infinities and NaN included.  bf16: fp32 scores, softmax
- * and sums; the weights are rounded to bf16 for the product with V.
+ * influence on it, infinities and NaN included; of those it does, a weight of
+ * 0 (a score of -infinity, or too far under the row's largest for fp32) times
+ * an infinite value is NaN.  A query whose every score is -infinity gets O = 0
+ * and lse = -infinity.  bf16: fp32 scores, softmax and sums; the weights are
+ * rounded to bf16 for the product with V.
  *
  * Q [tokens, Hq, d], K, V [key_tokens, Hkv, d] (dtype, read); cu_seqlens_q,
  * cu_seqlens_k [B + 1] int32 (device, read; the same array for plain

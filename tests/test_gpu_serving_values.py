@@ -1,0 +1,59 @@
+"""Infinite values under weights of 0 in the full causal attention.  The softmax is 32-bit: a key
+whose score is -infinity, or more than about 90 under the row's largest, has a weight of exactly 0,
+and 0 times infinity is NaN, wherever the key lies.  A row whose every score is -infinity has no
+weights at all: O = 0 and lse = -infinity."""
+import math
+
+import pytest
+import torch
+
+from tests import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _msa():
+    import block_sparse_long_03_b200 as msa
+    return msa
+
+
+def _prompt(dtype, n=300, Hq=4, d=64):
+    """Q, K, V with Q's channel 0 at 1 and K's at 0: it sets a key's score alone."""
+    g = torch.Generator().manual_seed(n)
+    Q, K, V = (torch.randn((n, H, d), generator=g).to(dtype).cuda() for H in (Hq, 1, 1))
+    Q[..., 0], K[..., 0] = 1.0, 0.0
+    return Q, K, V, ref.offsets([n]).cuda()
+
+
+@pytest.mark.parametrize("low", [-math.inf, -8.0 * 300])
+def test_infinite_value_under_a_zero_weight(low):
+    """Keys 5 and 140 have a weight of 0 in every row and an infinite value in one channel: NaN
+    there in every row that attends them (they are in tiles that some rows attend whole and others
+    in part), everything else bit for bit as with finite values."""
+    msa = _msa()
+    Q, K, V, cu = _prompt(BF16)
+    K[5, 0, 0] = K[140, 0, 0] = low
+    want, want_lse, _ = msa.attn_packed(Q, K, V, cu)
+    V[5, 0, 9], V[140, 0, 33] = math.inf, -math.inf
+    O, lse, _ = msa.attn_packed(Q, K, V, cu)
+    assert torch.equal(lse, want_lse)
+    odd = torch.zeros(O.shape, dtype=torch.bool, device="cuda")
+    odd[5:, :, 9] = True
+    odd[140:, :, 33] = True
+    assert bool(torch.isnan(O[odd]).all()), f"{O[odd][~torch.isnan(O[odd])][:4]}"
+    assert torch.equal(O[~odd], want[~odd])
+
+
+def test_rows_without_weights_ignore_infinite_values():
+    """The first rows' scores are all -infinity and their keys' values infinite: O = 0."""
+    msa = _msa()
+    Q, K, V, cu = _prompt(BF16)
+    K[:5, 0, 0] = -math.inf
+    V[:5, 0, 9], V[2, 0, 40] = math.inf, math.nan
+    O, lse, _ = msa.attn_packed(Q, K, V, cu)
+    assert bool((lse[:5] == -math.inf).all()) and bool((O[:5] == 0).all())
+    assert bool(torch.isnan(O[5:, :, 9]).all()) and bool(torch.isnan(O[5:, :, 40]).all())
+    keep = [c for c in range(64) if c not in (9, 40)]
+    assert bool(torch.isfinite(O[..., keep]).all()) and bool(torch.isfinite(lse[5:]).all())
