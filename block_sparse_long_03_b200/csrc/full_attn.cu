@@ -467,6 +467,12 @@ full_simt_kernel(FullShape s, FullSeqs sq, FullCut c, const FullPlan *plan, cons
             if (r >= rows) continue;
             float *dst = O + ((int64_t)(q.q0 + t0 + r / s.R) * s.Hq + g * s.R + r % s.R) * D;
             const float inv = inv_l[r];
+            // no weights (no key, or every score -infinity): 0, whatever the
+            // values were
+            if (inv == 0.f) {
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) acc[i][k] = 0.f;
+            }
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
                 *(float4 *)(dst + 4 * x + 32 * k) =

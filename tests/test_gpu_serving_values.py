@@ -57,3 +57,19 @@ def test_rows_without_weights_ignore_infinite_values():
     assert bool(torch.isnan(O[5:, :, 9]).all()) and bool(torch.isnan(O[5:, :, 40]).all())
     keep = [c for c in range(64) if c not in (9, 40)]
     assert bool(torch.isfinite(O[..., keep]).all()) and bool(torch.isfinite(lse[5:]).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp32_rows_without_weights_ignore_infinite_values(d):
+    """The same in fp32, and zero weights there."""
+    msa = _msa()
+    Q, K, V, cu = _prompt(F32, d=d)
+    K[:5, 0, 0] = K[140, 0, 0] = -math.inf
+    want, _, _ = msa.attn_packed(Q, K, V, cu)
+    V[:5, 0, 9], V[140, 0, 33] = math.inf, -math.inf
+    O, lse, _ = msa.attn_packed(Q, K, V, cu)
+    assert bool((lse[:5] == -math.inf).all()) and bool((O[:5] == 0).all())
+    odd = torch.zeros(O.shape, dtype=torch.bool, device="cuda")
+    odd[5:, :, 9] = True
+    odd[140:, :, 33] = True
+    assert bool(torch.isnan(O[odd]).all()) and torch.equal(O[~odd], want[~odd])
