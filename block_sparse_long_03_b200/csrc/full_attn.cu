@@ -231,7 +231,7 @@ __device__ __forceinline__ void add_parts(int i0, int parts, float mine, float m
     for (int u = 0; u < N; ++u) {
         l[u] = __shfl_sync(0xffffffffu, mine, (i0 + u) % 32);
         if (i0 + u >= parts) l[u] = -INFINITY;
-        // a part without a key of this row stored nothing
+        // a part without weights for this row may have stored nothing
         const bool use = l[u] != -INFINITY;
         const float *p = src + (i0 + u) * part_step;
         if constexpr (kPer == 4) {
@@ -289,6 +289,11 @@ full_combine_kernel(FullShape s, FullSeqs q, FullCut c, const FullPlan *plan, co
         if (i0 > 0 && i0 % 32 == 0)
             mine = i0 + lane < parts ? row_lse[(i0 + lane) * step] : -INFINITY;
         add_parts<N>(i0, parts, mine, m, src, step * D, sum, acc);
+    }
+    if (m == kNanPart && sum == sum) {                 // no part has weights
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
     }
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     __nv_bfloat162 o[kPer / 2];

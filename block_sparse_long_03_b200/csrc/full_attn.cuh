@@ -65,6 +65,11 @@ __host__ __device__ __forceinline__ int full_row_parts(const FullSeq &s, const F
     return n > 1 ? n : 0;
 }
 
+// The lse of a partial result whose weights are all 0 and whose O has a NaN (0
+// times an infinite value): the merge has to see it where other parts have
+// weights.  -infinity: nothing to add, and nothing may be stored.
+constexpr float kNanPart = -3.402823466e+38f;
+
 cudaError_t launch_full_plan(const FullShape &s, const FullSeqs &q, const FullCut &c,
                              FullPlan *plan, FullSeq *seqs, uint32_t *err, cudaStream_t st);
 // O and lse of the rows kept in parts: part_o [parts, tokens, Hq, d] fp32

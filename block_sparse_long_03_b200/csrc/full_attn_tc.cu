@@ -593,15 +593,40 @@ __device__ __forceinline__ float weights(const uint32_t (&v)[kHalf], uint32_t tP
     return x + y;
 }
 
-// The weight of key row k in query row q, against the running maximum m: for
-// an infinity or NaN among the values, which the products left out.  A weight
-// of 0 (a score of -infinity, or far below m) then gives NaN, as in a product.
-template <int D>
-__device__ __noinline__ float weight_of(const __nv_bfloat16 *q, const __nv_bfloat16 *k,
-                                        float scale_log2, float m) {
-    float dot = 0.f;
-    for (int c = 0; c < D; ++c) dot = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), dot);
-    return tc::ex2_approx(fmaf(dot, scale_log2, m == -INFINITY ? 0.f : -m * scale_log2));
+// Infinities and NaN among the values of keys lo .. hi, which the products left
+// out, enter one row's stored result (`out`, floats or bf16) with the weights
+// of their keys, worked out again against the running maximum m: a weight of
+// 0 (a score of -infinity, or far below m) gives NaN, as in a product.  Apart
+// from the epilogue's loop, and on its stores, so that the loop keeps its
+// registers.  Returns whether the row got a NaN.
+template <int D, bool kPaged, typename T>
+__device__ __noinline__ bool add_odd(const TcArgs &a, int b, int g, int64_t q_row, int head, int k0,
+                                     int lo, int hi, float m, T *out) {
+    const __nv_bfloat16 *q = a.Q + q_row * a.s.q_stride + (int64_t)(g * a.s.R + head) * D;
+    bool nan = false;
+    for (int j = lo; j <= hi; ++j) {
+        int64_t row = (int64_t)k0 + j;
+        if (kPaged)
+            row = (int64_t)a.q.block_table[(int64_t)b * a.s.max_pages + j / a.s.page_size] *
+                      a.s.page_size + j % a.s.page_size;
+        const __nv_bfloat16 *v = a.V + row * a.s.v_stride + (int64_t)g * D;
+        float p = -1.f;                                  // not worked out yet
+        for (int c = 0; c < D; ++c) {
+            const float f = __bfloat162float(v[c]);
+            if (isfinite(f)) continue;
+            if (p == -1.f) {
+                const __nv_bfloat16 *k = a.K + row * a.s.k_stride + (int64_t)g * D;
+                float dot = 0.f;
+                for (int e = 0; e < D; ++e)
+                    dot = fmaf(__bfloat162float(q[e]), __bfloat162float(k[e]), dot);
+                p = tc::ex2_approx(fmaf(dot, a.scale_log2, m == -INFINITY ? 0.f : -m * a.scale_log2));
+            }
+            const float x = fmaf(p, f, to_f32<T>(out[c]));
+            nan |= x != x;
+            out[c] = from_f32<T>(x);
+        }
+    }
+    return nan;
 }
 
 template <int D, bool kPaged>
@@ -688,16 +713,13 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
         if (h > 1) prev_phase ^= 1;
         if (busy && (w.pair || s == 0 || a.c.max_parts > 1)) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const float out_lse = l == 0.f ? -INFINITY : m * a.s.scale + logf(l);
             const int64_t at = (int64_t)(w.q0 + first_tok + tok) * a.s.Hq + w.g * a.s.R + head;
             const int64_t part = ((int64_t)w.part + (w.pair ? 0 : s)) * a.s.tokens * a.s.Hq + at;
             const bool odd = bar->odd[slot] == k + 1;
-            const bool some = __any_sync(0xffffffffu, valid && l != 0.f);
-            if (valid) {
-                if (w.parts > 0) a.part_lse[part] = out_lse;
-                else a.lse[at] = out_lse;
-            }
-            if (some || w.parts == 0) {
+            // no weights and nothing that a product with them could have made NaN
+            const bool zero = l == 0.f && (n == 0 || w.parts == 0);
+            bool nan = false;
+            if (n > 0 || w.parts == 0) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -708,30 +730,10 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                     }
                     float x[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
-                    if (odd && valid && l != 0.f) {
-                        const int hi = min(first_pos + tok, (t0 + n) * kFullKeys - 1);
-                        for (int jk = max(t0 * kFullKeys, w.pos0 + 1); jk <= hi; ++jk) {
-                            int64_t kr = (int64_t)w.k0 + jk;
-                            if (kPaged)
-                                kr = (int64_t)a.q.block_table[(int64_t)w.b * a.s.max_pages +
-                                                              jk / a.s.page_size] * a.s.page_size +
-                                     jk % a.s.page_size;
-                            const __nv_bfloat16 *vp = a.V + kr * a.s.v_stride + (int64_t)w.g * D + c;
-                            bool any = false;
-                            for (int i = 0; i < 32; ++i) any |= !isfinite(__bfloat162float(vp[i]));
-                            if (!any) continue;
-                            const float p = weight_of<D>(
-                                a.Q + (int64_t)(w.q0 + first_tok + tok) * a.s.q_stride +
-                                    (int64_t)(w.g * a.s.R + head) * D,
-                                a.K + kr * a.s.k_stride + (int64_t)w.g * D, a.scale_log2, m);
+                    for (int i = 0; i < 32; ++i) x[i] = zero ? 0.f : __uint_as_float(o[i]) * inv;
+                    if (l == 0.f) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float f = __bfloat162float(vp[i]);
-                                if (!isfinite(f)) x[i] = fmaf(p, f, x[i]);
-                            }
-                        }
+                        for (int i = 0; i < 32; ++i) nan |= x[i] != x[i];
                     }
                     if (valid && w.parts > 0) {
                         float *dst = a.part_o + part * D + c;
@@ -751,6 +753,21 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                         }
                     }
                 }
+            }
+            if (odd && valid && !zero) {
+                const int lo = max(t0 * kFullKeys, w.pos0 + 1);
+                const int hi = min(first_pos + tok, (t0 + n) * kFullKeys - 1);
+                const int64_t q_row = w.q0 + first_tok + tok;
+                nan |= w.parts > 0 ? add_odd<D, kPaged>(a, w.b, w.g, q_row, head, w.k0, lo, hi, m,
+                                                        a.part_o + part * D)
+                                   : add_odd<D, kPaged>(a, w.b, w.g, q_row, head, w.k0, lo, hi, m,
+                                                        a.O + at * D);
+            }
+            if (valid) {
+                const float out_lse = l != 0.f ? m * a.s.scale + logf(l)
+                                               : nan ? kNanPart : -INFINITY;
+                if (w.parts > 0) a.part_lse[part] = out_lse;
+                else a.lse[at] = out_lse;
             }
             tc::tc_fence_before();
         }

@@ -73,3 +73,31 @@ def test_fp32_rows_without_weights_ignore_infinite_values(d):
     odd[5:, :, 9] = True
     odd[140:, :, 33] = True
     assert bool(torch.isnan(O[odd]).all()) and torch.equal(O[~odd], want[~odd])
+
+
+def test_zero_weights_of_a_whole_key_run():
+    """Single tokens over keys that are cut into runs.  A whole run (1024 keys) of scores of
+    -infinity with an infinite value in it: NaN in that channel, the other channels as with finite
+    values; without an infinite value nothing changes.  Every key so: O = 0."""
+    msa, g = _msa(), torch.Generator().manual_seed(7)
+    Hq, d, page, L = 2, 64, 64, [4096, 4096, 3000]
+    _, _, Kc, Vc, table = ref.paginate(L, page, 1, 1, d, BF16, g, "cuda", math.nan)
+    Q = torch.randn((3, Hq, d), generator=g).to(BF16).cuda()
+    Q[..., 0] = 1.0
+    run = table[0, 16:32].long()                       # keys 1024 .. 2047 of the first
+    Kc[run, :, :, 0] = -math.inf
+    Kc[table[2, :47].long(), :, :, 0] = -math.inf      # every key of the third
+    args = (Q, Kc, Vc, ref.offsets([1, 1, 1]).cuda(), torch.tensor(L, dtype=torch.int32).cuda(),
+            table)
+    want, want_lse, ws = msa.attn_paged(*args)
+    assert msa.msa_get_device_error(ws) == 0 and bool(torch.isfinite(want).all())
+    for at in (16, 24, 31):
+        Vc2 = Vc.clone()
+        Vc2[table[0, at].long(), 5, 0, 9] = math.inf
+        Vc2[table[2, at].long(), 5, 0, 9] = math.inf
+        O, lse, _ = msa.attn_paged(Q, Kc, Vc2, *args[3:])
+        assert torch.equal(lse, want_lse)
+        assert bool(torch.isnan(O[0, :, 9]).all()), at
+        assert bool((O[2] == 0).all()) and bool((lse[2] == -math.inf).all())
+        O[0, :, 9] = want[0, :, 9]
+        assert torch.equal(O, want)
