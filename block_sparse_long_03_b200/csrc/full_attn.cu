@@ -97,12 +97,13 @@ full_plan_kernel(FullShape s, FullSeqs q, FullCut c, FullPlan *plan, FullSeq *se
         return;
     }
     // lengths; a paged sequence with a length outside [T, capacity] or a bad
-    // page id gets L = 0
+    // page id gets L = 0, and so does one without queries, whose length and
+    // pages nothing reads (an idle slot may hold anything)
     for (int b = tid; b < s.B; b += kPlanThreads) {
         const int32_t q0 = q.cu_q[b], T = q.cu_q[b + 1] - q0;
         int32_t L, k0 = 0;
         if (s.paged) {
-            L = q.seq_lens[b];
+            L = T > 0 ? q.seq_lens[b] : 0;
             if (L < T || (int64_t)L > (int64_t)s.max_pages * s.page_size) {
                 L = 0;
                 record_error(err, MSA_ERR_BAD_PAGE_TABLE, 3);

@@ -559,6 +559,8 @@ MSA_EXPORT msa_status_t msa_attn_packed(const msa_attn_params_t *params, const v
  * A sequence with L_b < T_b, L_b > max_pages * page_size or a page id outside
  * [0, num_pages) among its first ceil(L_b / page_size) is skipped: its O is
  * 0, its lse -infinity, and the error word records MSA_ERR_BAD_PAGE_TABLE.
+ * The length and pages of a sequence without new tokens are not looked at (nor
+ * does msa_rope_append_paged look at them).
  * Bad offsets: as msa_attn_packed.
  */
 MSA_EXPORT msa_status_t msa_attn_paged(const msa_attn_params_t *params, const void *Q,

@@ -1,7 +1,8 @@
-"""Infinite values under weights of 0 in the full causal attention.  The softmax is 32-bit: a key
-whose score is -infinity, or more than about 90 under the row's largest, has a weight of exactly 0,
-and 0 times infinity is NaN, wherever the key lies.  A row whose every score is -infinity has no
-weights at all: O = 0 and lse = -infinity."""
+"""Values and slots that must not count in the full causal attention, and infinite values that do.
+
+The softmax is 32-bit: a key whose score is -infinity, or more than about 90 under the row's
+largest, has a weight of exactly 0, and 0 times infinity is NaN, wherever the key lies.  A row
+whose every score is -infinity has no weights at all: O = 0 and lse = -infinity."""
 import math
 
 import pytest
@@ -101,3 +102,31 @@ def test_zero_weights_of_a_whole_key_run():
         assert bool((O[2] == 0).all()) and bool((lse[2] == -math.inf).all())
         O[0, :, 9] = want[0, :, 9]
         assert torch.equal(O, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_idle_slots_may_hold_anything(dtype):
+    """Sequences without new tokens, with stale lengths and page ids, between sequences that have
+    some: no error is recorded by the attention or by the cache write, and the outputs are those of
+    the batch without them."""
+    msa, g = _msa(), torch.Generator().manual_seed(19)
+    T, L, page, Hq, Hkv, d = [2, 0, 1, 0, 0, 40, 0], [70, 50, 300, 9, 17, 64, 33], 16, 4, 2, 64
+    Ks, Vs, Kc, Vc, table = ref.paginate(L, page, 1, Hkv, d, dtype, g, "cuda", math.nan)
+    lens = torch.tensor(L, dtype=torch.int32)
+    lens[1], lens[3], lens[4] = -7, page * table.shape[1] + 1, (1 << 31) - 1
+    table[1, :], table[3, 0], table[6, 1] = -1, Kc.shape[0], 1 << 30
+    Q = torch.randn((sum(T), Hq, d), generator=g).to(dtype).cuda()
+    cu = ref.offsets(T)
+    O, lse, ws = msa.attn_paged(Q, Kc, Vc, cu.cuda(), lens.cuda(), table)
+    assert msa.msa_get_device_error(ws) == 0
+    for b in (0, 2, 5):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        ref.assert_attention(O[rows], lse[rows],
+                             ref.attention(Q[rows], Ks[b].cuda(), Vs[b].cuda()), f"sequence {b}")
+    K, V = (torch.randn((sum(T), Hkv, d), generator=g).to(dtype).cuda() for _ in range(2))
+    _, ws = msa.rope_append_paged(Q, K, V, None, cu.cuda(), lens.cuda(), table,
+                                  msa.rope_frequencies(d), Kc, Vc)
+    assert msa.msa_get_device_error(ws) == 0
+    empty = torch.zeros_like(cu).cuda()                # a batch of idle slots alone
+    O, _, ws = msa.attn_paged(Q[:0], Kc, Vc, empty, lens.cuda(), table)
+    assert msa.msa_get_device_error(ws) == 0
