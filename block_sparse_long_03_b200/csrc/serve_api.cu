@@ -246,7 +246,8 @@ msa_status_t msa_rope_append_paged(
     if (!stride_ok(v_stride, (int64_t)params->Hkv * params->d, params->tokens, params->dtype))
         return MSA_ERR_INVALID_ARG;
     if (k_idx != nullptr && (d_idx % 16 != 0 || d_idx > 128)) return MSA_ERR_UNSUPPORTED;
-    if ((int64_t)max_pages * page_size > 0x7fffff00ll) return MSA_ERR_UNSUPPORTED;
+    // sequences and key positions are counted in 32 bits, in steps of 256 and 32
+    if (B > 0x7fffff00 || (int64_t)max_pages * page_size > 0x7fffff00ll) return MSA_ERR_UNSUPPORTED;
     if (!workspace || ((uintptr_t)workspace % kAlign) != 0 || workspace_bytes < kErrorBytes)
         return MSA_ERR_WORKSPACE;
     AppendArgs c;

@@ -487,6 +487,7 @@ MSA_EXPORT msa_status_t msa_rope(const msa_rope_params_t *params, const void *Q,
  * checks the offsets.
  * seq_lens, block_table, page_size, max_pages, num_pages and the caches: as
  * msa_decode_paged.  Two tokens must not have the same cache row.
+ * B and max_pages * page_size are at most 2^31 - 256.
  * workspace: at least 256 bytes, 256-byte aligned: the device error word.
  *
  * Lengths and page ids are checked on the device: a token whose sequence
