@@ -100,6 +100,9 @@ msa_status_t make_full(const msa_attn_params_t *p, bool paged, FullShape *s) {
         !stride_ok(s->k_stride, dk, s->key_tokens, s->dtype) ||
         !stride_ok(s->v_stride, dk, s->key_tokens, s->dtype))
         return MSA_ERR_INVALID_ARG;
+    // the strides of a tensor map are under 2^40 bytes
+    if (s->dtype == MSA_BF16 && std::max({s->q_stride, s->k_stride, s->v_stride}) * 2 >= 1ll << 40)
+        return MSA_ERR_UNSUPPORTED;
     s->paged = paged;
     s->page_size = p->page_size; s->max_pages = p->max_pages; s->num_pages = p->num_pages;
     return MSA_OK;

@@ -506,7 +506,8 @@ typedef struct {
     int64_t tokens;      /* rows of Q, O and lse, <= 2^31 - 256                  */
     int64_t key_tokens;  /* rows of packed K and V, <= 2^31 - 256 (paged calls:  */
                          /* not read)                                            */
-    int64_t q_stride, k_stride, v_stride;   /* paged calls read q_stride only    */
+    int64_t q_stride, k_stride, v_stride;   /* paged calls read q_stride only;   */
+                         /* bf16: under 2^40 bytes each                          */
     int32_t B;           /* sequences                                            */
     int32_t Hq, Hkv;     /* heads; Hq % Hkv == 0, Hq / Hkv <= 64                 */
     int32_t d;           /* head dimension: 64 or 128                            */
