@@ -25,6 +25,54 @@ bool stride_ok(int64_t &stride, int64_t dense, int64_t tokens, int dtype) {
     return (double)stride * (double)std::max<int64_t>(tokens, 1) < 4e18 / 4;
 }
 
+// Memory that a call reads or writes: n rows of `row` bytes, `step` bytes from
+// one to the next.
+struct Span {
+    int64_t at, row, step, n;
+    int64_t end() const { return at + (n - 1) * step + row; }
+};
+Span rows_of(const void *p, int64_t n, int64_t row, int64_t step) {
+    if (p == nullptr || row <= 0) n = 0;
+    if (step == row && n > 1) return Span{(int64_t)(uintptr_t)p, row * n, row * n, 1};
+    return Span{(int64_t)(uintptr_t)p, row, step, n};
+}
+Span bytes_of(const void *p, double bytes) {             // (more than memory holds: as much as that)
+    const int64_t n = (int64_t)std::min(bytes, (double)(1ll << 56));
+    return rows_of(p, 1, n, n);
+}
+// Some row of b overlaps row i of a.
+bool row_meets(const Span &a, int64_t i, const Span &b) {
+    const int64_t x = a.at + i * a.step, past = x - b.at - b.row;
+    const int64_t j = past < 0 ? 0 : past / b.step + 1;   // the first row of b that ends behind x
+    return j < b.n && b.at + j * b.step < x + a.row;
+}
+// Two spans share a byte.  Slices of one fused tensor have equal steps: which
+// rows meet depends on the distance of their numbers alone, and those of all
+// distances are among the first row of one against the other.
+bool overlap(const Span &a, const Span &b) {
+    if (a.n <= 0 || b.n <= 0 || a.end() <= b.at || b.end() <= a.at) return false;
+    if (a.step == b.step) return row_meets(a, 0, b) || row_meets(b, 0, a);
+    if (a.n > b.n) return overlap(b, a);
+    for (int64_t i = 0; i < a.n; ++i)
+        if (row_meets(a, i, b)) return true;
+    return false;
+}
+// An output overlaps an input or another output.
+template <int kOut, int kIn>
+bool outputs_overlap(const Span (&out)[kOut], const Span (&in)[kIn]) {
+    for (int o = 0; o < kOut; ++o) {
+        for (int i = 0; i < kIn; ++i)
+            if (overlap(out[o], in[i])) return true;
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[o], out[i])) return true;
+    }
+    return false;
+}
+// An output that overlaps its input is the input, with its stride.
+bool in_place_or_apart(const Span &out, const Span &in) {
+    return (out.at == in.at && out.row == in.row && out.step == in.step) || !overlap(out, in);
+}
+
 // Validate and convert the rotary parameters; Hq or Hkv becomes 0 where the
 // tensor is NULL.
 msa_status_t make_rope(const msa_rope_params_t *p, const void *Q, const void *Q_out, const void *K,
@@ -67,6 +115,18 @@ msa_status_t make_rope(const msa_rope_params_t *p, const void *Q, const void *Q_
     a->mscale = p->mscale;
     return MSA_OK;
 }
+
+// The tokens of a call with such parameters.
+struct RopeSpans {
+    Span q, k, q_out, k_out;
+    RopeSpans(const RopeArgs &a, int dtype) {
+        const int64_t e = elem(dtype), dq = (int64_t)a.Hq * a.d * e, dk = (int64_t)a.Hkv * a.d * e;
+        q = rows_of(a.Q, a.tokens, dq, a.q_stride * e);
+        k = rows_of(a.K, a.tokens, dk, a.k_stride * e);
+        q_out = rows_of(a.Q_out, a.tokens, dq, a.qo_stride * e);
+        k_out = rows_of(a.K_out, a.tokens, dk, a.ko_stride * e);
+    }
+};
 
 // Validate an attention call's sizes.
 msa_status_t make_full(const msa_attn_params_t *p, bool paged, FullShape *s) {
@@ -153,24 +213,33 @@ msa_status_t run_full(const msa_attn_params_t *params, bool paged, const void *Q
     if (!workspace || ((uintptr_t)workspace % kAlign) != 0 || workspace_bytes < L.total)
         return MSA_ERR_WORKSPACE;
     // a row may be written while another row's inputs are still read
-    if (s.tokens > 0 && (O == Q || O == K || O == V || O == lse)) return MSA_ERR_INVALID_ARG;
+    const int64_t e = elem(s.dtype), dq = (int64_t)s.Hq * s.d * e, dk = (int64_t)s.Hkv * s.d * e;
+    const Span out[] = {bytes_of(O, (double)s.tokens * dq), bytes_of(lse, 4.0 * s.tokens * s.Hq),
+                        bytes_of(workspace, (double)L.total)};
+    const Span in[] = {rows_of(Q, s.tokens, dq, s.q_stride * e),
+                       rows_of(K, s.key_tokens, dk, s.k_stride * e),
+                       rows_of(V, s.key_tokens, dk, s.v_stride * e),
+                       bytes_of(q.cu_q, 4.0 * (s.B + 1)), bytes_of(q.cu_k, 4.0 * (s.B + 1)),
+                       bytes_of(q.seq_lens, 4.0 * s.B),
+                       bytes_of(q.block_table, 4.0 * s.B * s.max_pages)};
+    if (outputs_overlap(out, in)) return MSA_ERR_INVALID_ARG;
     char *ws = (char *)workspace;
     uint32_t *err = (uint32_t *)ws;
     FullPlan *plan = (FullPlan *)(ws + L.plan);
     FullSeq *seqs = (FullSeq *)(ws + L.seqs);
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = launch_full_plan(s, q, c, plan, seqs, err, st);
-    if (s.tokens == 0) return cuda_status(e);
+    cudaError_t done = launch_full_plan(s, q, c, plan, seqs, err, st);
+    if (s.tokens == 0) return cuda_status(done);
     if (s.dtype == MSA_F32) {
-        if (e == cudaSuccess) e = launch_full_simt(s, q, c, plan, seqs, Q, K, V, O, lse, st);
-        return cuda_status(e);
+        if (done == cudaSuccess) done = launch_full_simt(s, q, c, plan, seqs, Q, K, V, O, lse, st);
+        return cuda_status(done);
     }
     float *part_o = (float *)(ws + L.part_o), *part_lse = (float *)(ws + L.part_lse);
-    if (e == cudaSuccess)
-        e = launch_full_tc(s, q, c, plan, seqs, Q, K, V, O, lse, part_o, part_lse, err, st);
-    if (e == cudaSuccess && c.max_parts > 1)
-        e = launch_full_combine(s, q, c, plan, seqs, part_o, part_lse, O, lse, st);
-    return cuda_status(e);
+    if (done == cudaSuccess)
+        done = launch_full_tc(s, q, c, plan, seqs, Q, K, V, O, lse, part_o, part_lse, err, st);
+    if (done == cudaSuccess && c.max_parts > 1)
+        done = launch_full_combine(s, q, c, plan, seqs, part_o, part_lse, O, lse, st);
+    return cuda_status(done);
 }
 
 }  // namespace
@@ -214,6 +283,13 @@ msa_status_t msa_rope(const msa_rope_params_t *params, const void *Q, const void
     if (rc != MSA_OK) return rc;
     if (positions == nullptr || ((uintptr_t)positions & 3u) != 0) return MSA_ERR_INVALID_ARG;
     a.positions = positions;
+    const RopeSpans r(a, params->dtype);
+    const Span out[] = {r.q_out, r.k_out};
+    const Span in[] = {bytes_of(positions, 4.0 * a.tokens), bytes_of(inv_freq, 4.0 * a.rot)};
+    if (a.tokens > 0 &&
+        (outputs_overlap(out, in) || !in_place_or_apart(r.q_out, r.q) ||
+         !in_place_or_apart(r.k_out, r.k) || overlap(r.q_out, r.k) || overlap(r.k_out, r.q)))
+        return MSA_ERR_INVALID_ARG;
     return cuda_status(launch_rope(a, params->dtype, params->layout == MSA_ROPE_INTERLEAVED,
                                    (cudaStream_t)stream));
 }
@@ -253,6 +329,18 @@ msa_status_t msa_rope_append_paged(
     if (B > 0x7fffff00 || (int64_t)max_pages * page_size > 0x7fffff00ll) return MSA_ERR_UNSUPPORTED;
     if (!workspace || ((uintptr_t)workspace % kAlign) != 0 || workspace_bytes < kErrorBytes)
         return MSA_ERR_WORKSPACE;
+    const RopeSpans r(a, params->dtype);
+    const int64_t e = elem(params->dtype), dk = (int64_t)params->Hkv * params->d * e, n = a.tokens;
+    const double rows = (double)num_pages * page_size;
+    const Span out[] = {r.q_out, bytes_of(K_cache, rows * dk), bytes_of(V_cache, rows * dk),
+                        bytes_of(k_idx_cache, rows * d_idx * e), bytes_of(workspace, kErrorBytes)};
+    const Span in[] = {r.k, rows_of(V, n, dk, v_stride * e),
+                       bytes_of(k_idx, (double)n * d_idx * e), bytes_of(cu_seqlens, 4.0 * (B + 1.0)),
+                       bytes_of(seq_lens, 4.0 * B), bytes_of(block_table, 4.0 * B * max_pages),
+                       bytes_of(inv_freq, 4.0 * a.rot)};
+    if (outputs_overlap(out, in) || !in_place_or_apart(r.q_out, r.q)) return MSA_ERR_INVALID_ARG;
+    for (int i = 1; i < 5; ++i)
+        if (overlap(out[i], r.q)) return MSA_ERR_INVALID_ARG;
     AppendArgs c;
     c.cu_seqlens = cu_seqlens; c.seq_lens = seq_lens; c.block_table = block_table;
     c.V = V; c.k_idx = k_idx; c.V_cache = V_cache; c.k_idx_cache = k_idx_cache;

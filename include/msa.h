@@ -464,8 +464,9 @@ typedef struct {
  * Q [tokens, Hq, d], K [tokens, Hkv, d] (dtype, read); positions [tokens]
  * int32 (read; any value, negative ones too); inv_freq [rot_dim / 2] FLOAT64
  * (device, read); Q_out, K_out (written).  An output may be its input
- * (with the same stride); other overlaps are not allowed.  Either pair (Q,
- * Q_out) or (K, K_out) may be NULL, NULL.  tokens may be 0.
+ * (with the same stride); any other overlap of an output with an input or
+ * with the other output is refused.  Either pair (Q, Q_out) or (K, K_out) may
+ * be NULL, NULL.  tokens may be 0.
  */
 MSA_EXPORT msa_status_t msa_rope(const msa_rope_params_t *params, const void *Q, const void *K,
                                  const int32_t *positions, const double *inv_freq, void *Q_out,
@@ -487,6 +488,8 @@ MSA_EXPORT msa_status_t msa_rope(const msa_rope_params_t *params, const void *Q,
  * checks the offsets.
  * seq_lens, block_table, page_size, max_pages, num_pages and the caches: as
  * msa_decode_paged.  Two tokens must not have the same cache row.
+ * Q_out may be Q (with the same stride); any other overlap of Q_out, the
+ * caches and the workspace with an input or with one another is refused.
  * B and max_pages * page_size are at most 2^31 - 256.
  * workspace: at least 256 bytes, 256-byte aligned: the device error word.
  *
@@ -537,9 +540,10 @@ MSA_EXPORT size_t msa_attn_workspace_size(const msa_attn_params_t *params, int p
  * Q [tokens, Hq, d], K, V [key_tokens, Hkv, d] (dtype, read); cu_seqlens_q,
  * cu_seqlens_k [B + 1] int32 (device, read; the same array for plain
  * prompts); O [tokens, Hq, d] dense (dtype, written), lse [tokens, Hq]
- * float32 (written); neither may overlap an input.  workspace: msa_attn_workspace_size(params, 0) bytes,
+ * float32 (written).  workspace: msa_attn_workspace_size(params, 0) bytes,
  * 256-byte aligned, used by one call at a time; first 256 bytes: the device
- * error word.
+ * error word.  An overlap of O, lse or the workspace with an input or with one
+ * another is refused (MSA_ERR_INVALID_ARG).
  *
  * Offsets that descend or leave the arrays are found on the device: no row
  * is written then, and the error word records MSA_ERR_BAD_OFFSETS.

@@ -130,3 +130,32 @@ def test_idle_slots_may_hold_anything(dtype):
     empty = torch.zeros_like(cu).cuda()                # a batch of idle slots alone
     O, _, ws = msa.attn_paged(Q[:0], Kc, Vc, empty, lens.cuda(), table)
     assert msa.msa_get_device_error(ws) == 0
+
+
+def test_outputs_between_the_rows_of_inputs():
+    """Outputs that share a buffer with inputs but no byte are not refused: in-place turns of two
+    slices, turned rows between the rows of Q, and O inside the gap of a strided Q."""
+    msa, g = _msa(), torch.Generator().manual_seed(23)
+    n, H, d = 33, 2, 64
+    f, pos = msa.rope_frequencies(d), torch.arange(n, dtype=torch.int32, device="cuda")
+    room = torch.randn((2 * n, H, d), generator=g).to(BF16).cuda()
+    Q, out = room[::2], room[1::2]
+    want, _ = msa.rope(Q.contiguous(), None, pos, f)
+    got, _ = msa.rope(Q, None, pos, f, Q_out=out)
+    assert got.data_ptr() == out.data_ptr() and torch.equal(out, want)
+    room = torch.randn((n, 3 * H, d), generator=g).to(BF16).cuda()
+    before = room.clone()
+    msa.rope(room[:, :H], room[:, 2 * H:], pos, f, Q_out=room[:, H:2 * H], K_out=room[:, 2 * H:])
+    want = msa.rope(before[:, :H].contiguous(), before[:, 2 * H:].contiguous(), pos, f)
+    assert torch.equal(room[:, :H], before[:, :H])
+    assert torch.equal(room[:, H:2 * H], want[0]) and torch.equal(room[:, 2 * H:], want[1])
+    wide = torch.randn((2, 64 * H, d), generator=g).to(BF16).cuda()     # other strides on each side
+    Q, out = wide[:, :H], wide[0, H:5 * H].view(2, 2 * H, d)[:, :H]
+    want, _ = msa.rope(Q.contiguous(), None, pos[:2], f)
+    msa.rope(Q, None, pos[:2], f, Q_out=out)
+    assert torch.equal(out, want)
+    O = wide[0, 5 * H:7 * H].view(2, H, d)
+    cu = ref.offsets([2]).cuda()
+    want = msa.attn_packed(Q.contiguous(), Q.contiguous(), Q.contiguous(), cu)[0]
+    msa.attn_packed(Q, Q, Q, cu, out=O)
+    assert torch.equal(O, want)
