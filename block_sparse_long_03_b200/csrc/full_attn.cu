@@ -531,7 +531,7 @@ cudaError_t launch_full_combine(const FullShape &s, const FullSeqs &q, const Ful
                         (__nv_bfloat16 *)O, lse);
 }
 
-FullCut full_simt_cut(const FullShape &s) { return FullCut{kSimtRows / s.R, 0, 0, 1, 1}; }
+FullCut full_simt_cut(const FullShape &s) { return FullCut{kSimtRows / s.R, 0, 0, 1, 1, 0}; }
 
 cudaError_t launch_full_simt(const FullShape &s, const FullSeqs &q, const FullCut &c,
                              const FullPlan *plan, const FullSeq *seqs, const void *Q,

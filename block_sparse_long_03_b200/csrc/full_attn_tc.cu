@@ -54,6 +54,14 @@ constexpr int kRows = 128;               // rows of a row tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaxLag = 8.f;           // log2 of how far P may pass 1
 constexpr int kHalf = 64;                // keys of one S / P buffer
+constexpr int kMaxCtas = 148;            // SMs of a B200
+
+// Halves whose products are summed in TMEM before O and the row sum move to
+// fp32 sums in memory.  The tensor core adds to its fp32 sums four keys at a time
+// and cuts the result off, towards 0: over 2^20 keys at once O came out 0.66 %
+// too small, over 2^22 2.6 %, over 2^26 a third; over 2^16, this many, 0.04 %,
+// a tenth of bf16's rounding.
+constexpr int kFoldHalves = 1024;
 
 template <int D> constexpr int ring_slots() { return D == 128 ? 5 : 10; }
 template <int D> constexpr size_t tc_smem() {
@@ -70,6 +78,7 @@ struct TcArgs {
     const __nv_bfloat16 *Q, *K, *V;      // Q, K: read for infinite values' weights only
     __nv_bfloat16 *O;
     float *lse, *part_o, *part_lse;
+    float *fold;                         // [CTA][stream][row][d + 4]: earlier sums of O, of weights
     uint32_t *err;
     int box;                             // key rows of one TMA box
     bool wide;                           // O is 32-byte aligned
@@ -387,7 +396,7 @@ __device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ,
 #pragma unroll
             for (int c = 0; c < kHalf / 16; ++c)
                 tc::mma_ts(tO, tS + b * kHalf + c * 8, desc(va + (b * 4 + c) * 128), idesc_o,
-                           (i > 0 || c > 0) ? 1u : 0u);
+                           (i % kFoldHalves > 0 || c > 0) ? 1u : 0u);
             if (i + 2 == h) tc::mma_commit(&bar->o_prev[me]);
             if (i + 1 == h) tc::mma_commit(&bar->o_full[me]);
             return true;
@@ -629,6 +638,52 @@ __device__ __noinline__ bool add_odd(const TcArgs &a, int b, int g, int64_t q_ro
     return nan;
 }
 
+// The earlier sums of a row of this CTA's stream s.
+template <int D>
+__device__ __forceinline__ float *fold_sums(const TcArgs &a, int s, int row) {
+    return a.fold + ((blockIdx.x * 2 + s) * (int64_t)kRows + row) * (D + 4);
+}
+// O and the sum of weights l so far join the row's earlier sums (none yet where
+// `first`).
+template <int D>
+__device__ __noinline__ void fold_in(uint32_t tO, float *sums, float l, bool first) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        tc::tmem_ld32(tO + c, o);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            float4 *at = (float4 *)(sums + c + i);
+            float4 v = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *at;
+            v.x += __uint_as_float(o[i]);
+            v.y += __uint_as_float(o[i + 1]);
+            v.z += __uint_as_float(o[i + 2]);
+            v.w += __uint_as_float(o[i + 3]);
+            *at = v;
+        }
+    }
+    sums[D] = (first ? 0.f : sums[D]) + l;
+}
+// The earlier sums join O; returns their sum of weights.
+template <int D>
+__device__ __noinline__ float fold_out(uint32_t tO, const float *sums) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        tc::tmem_ld32(tO + c, o);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) + sums[c + i]);
+        tc::tmem_st32(tO + c, o);
+    }
+    tc::tmem_st_wait();
+    return sums[D];
+}
+
 template <int D, bool kPaged>
 __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
     const int quad = (threadIdx.x / 32) % 4, lane = threadIdx.x % 32;
@@ -650,59 +705,75 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
         const int first_pos = w.pos0 + first_tok;        // of the stream's first token
         const int t0 = stream_a(w, s), h = stream_h(w, s), n = (h + 1) / 2;
         float m = -INFINITY, l = 0.f;
-        for (int i = 0; i < h; ++i) {
-            const int b = i & 1;
-            const uint32_t tB = tS + b * kHalf;
-            if (!tc::mbar_wait(&bar->s_full[s][b], (s_phase >> b) & 1, a.err, &bar->abort)) return;
-            s_phase ^= 1u << b;
-            if (busy) {
+        // P V of halves i - 1 and before is in O once S(i + 1), issued after it,
+        // is complete; at the last half o_prev tells
+        auto products_done = [&](int i) {
+            const int b = (i + 1) & 1;
+            return i + 1 < h ? tc::mbar_wait(&bar->s_full[s][b], (s_phase >> b) & 1, a.err, &bar->abort)
+                             : tc::mbar_wait(&bar->o_prev[s], prev_phase, a.err, &bar->abort);
+        };
+        for (int i0 = 0; i0 < h; i0 += kFoldHalves) {
+            const int end = min(h, i0 + kFoldHalves);
+            if (i0 > 0 && busy) {                        // the next product starts O anew
+                if (!products_done(i0)) return;
                 tc::tc_fence_after();
-                uint32_t v[kHalf];
-                tc::tmem_ld32(tB, *(uint32_t(*)[32])v);
-                tc::tmem_ld32(tB + 32, *(uint32_t(*)[32])(v + 32));
-                tc::tmem_ld_wait();
-                const int key0 = t0 * kFullKeys + i * kHalf;
-                const bool edge = key0 + kHalf > first_pos + 1;
-                if (edge) {
-                    const int lim = first_pos + tok - key0;   // columns above lim are not attended
-#pragma unroll
-                    for (int c = 0; c < kHalf; ++c)
-                        if (c > lim) v[c] = __float_as_uint(-INFINITY);
-                }
-                const float top = row_max(v);
-                const bool move = valid && !(top <= m + a.lag);   // (a NaN moves m too)
-                if (i == 0) {
-                    m = top;
-                } else if (__any_sync(0xffffffffu, move)) {
-                    // O is rescaled between the products of halves i - 1 and
-                    // i.  The first is complete once S(i + 1), issued after
-                    // it, is; at the last half o_prev tells.
-                    if (i + 1 < h ? !tc::mbar_wait(&bar->s_full[s][b ^ 1], (s_phase >> (b ^ 1)) & 1,
-                                                   a.err, &bar->abort)
-                                  : !tc::mbar_wait(&bar->o_prev[s], prev_phase, a.err, &bar->abort))
-                        return;
-                    tc::tc_fence_after();
-                    const float f = move ? tc::ex2_approx((m - top) * a.scale_log2) : 1.f;
-                    if (move) m = top;
-                    l *= f;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tc::tmem_ld32(tO + c, o);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc::tmem_st32(tO + c, o);
-                    }
-                }
-                const float mb = m == -INFINITY ? 0.f : -m * a.scale_log2;
-                l += weights(v, tB, scale2, pack2(mb, mb));
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
+                fold_in<D>(tO, fold_sums<D>(a, s, row), l, i0 == kFoldHalves);
+                l = 0.f;
             }
-            __syncwarp();
-            arrive_if(lane == 0, &bar->p_full[s][b]);
+            for (int i = i0; i < end; ++i) {
+                const int b = i & 1;
+                const uint32_t tB = tS + b * kHalf;
+                if (!tc::mbar_wait(&bar->s_full[s][b], (s_phase >> b) & 1, a.err, &bar->abort)) return;
+                s_phase ^= 1u << b;
+                if (busy) {
+                    tc::tc_fence_after();
+                    uint32_t v[kHalf];
+                    tc::tmem_ld32(tB, *(uint32_t(*)[32])v);
+                    tc::tmem_ld32(tB + 32, *(uint32_t(*)[32])(v + 32));
+                    tc::tmem_ld_wait();
+                    const int key0 = t0 * kFullKeys + i * kHalf;
+                    const bool edge = key0 + kHalf > first_pos + 1;
+                    if (edge) {
+                        const int lim = first_pos + tok - key0;   // columns above lim are not attended
+#pragma unroll
+                        for (int c = 0; c < kHalf; ++c)
+                            if (c > lim) v[c] = __float_as_uint(-INFINITY);
+                    }
+                    const float top = row_max(v);
+                    const bool move = valid && !(top <= m + a.lag);   // (a NaN moves m too)
+                    if (i == 0) {
+                        m = top;
+                    } else if (__any_sync(0xffffffffu, move)) {
+                        // O is rescaled between the products of halves i - 1 and i
+                        if (!products_done(i)) return;
+                        tc::tc_fence_after();
+                        const float f = move ? tc::ex2_approx((m - top) * a.scale_log2) : 1.f;
+                        if (move) m = top;
+                        l *= f;
+                        if (i0 > 0) {
+                            float *x = fold_sums<D>(a, s, row);
+#pragma unroll 1
+                            for (int c = 0; c <= D; ++c) x[c] *= f;
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tc::tmem_ld32(tO + c, o);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc::tmem_st32(tO + c, o);
+                        }
+                    }
+                    const float mb = m == -INFINITY ? 0.f : -m * a.scale_log2;
+                    l += weights(v, tB, scale2, pack2(mb, mb));
+                    tc::tmem_st_wait();
+                    tc::tc_fence_before();
+                }
+                __syncwarp();
+                arrive_if(lane == 0, &bar->p_full[s][b]);
+            }
         }
         // epilogue: O / l and the log-sum-exp, final or as one of the row's parts
         if (h > 0) {
@@ -712,6 +783,7 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
         }
         if (h > 1) prev_phase ^= 1;
         if (busy && (w.pair || s == 0 || a.c.max_parts > 1)) {
+            if (h > kFoldHalves) l += fold_out<D>(tO, fold_sums<D>(a, s, row));
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int64_t at = (int64_t)(w.q0 + first_tok + tok) * a.s.Hq + w.g * a.s.R + head;
             const int64_t part = ((int64_t)w.part + (w.pair ? 0 : s)) * a.s.tokens * a.s.Hq + at;
@@ -880,7 +952,7 @@ cudaError_t launch_tc_t(const FullShape &s, const TcArgs &a, const void *Q, cons
     const int64_t most = (s.tokens / a.c.unit_tokens + std::min<int64_t>(s.B, s.tokens)) * s.Hkv *
                          a.c.max_parts;
     count_launches(1);
-    return launch_after(full_tc_kernel<D, kPaged>, dim3((unsigned)std::min<int64_t>(most, sms)),
+    return launch_after(full_tc_kernel<D, kPaged>, dim3((unsigned)std::min<int64_t>(most, std::min(sms, kMaxCtas))),
                         dim3(kThreads), tc_smem<D>(), st, tq, tq1, tk, tv, a);
 }
 
@@ -896,13 +968,15 @@ cudaError_t launch_tc_t(const FullShape &s, const TcArgs &a, const void *Q, cons
 // shortest then need no merge (28.7 against 32.8 us).  The partial results
 // take at most (items + units) * 256 rows * 2, about 300 MB.
 FullCut full_tc_cut(const FullShape &s) {
-    constexpr int kItemsPerSm = 4, kSms = 148;
+    constexpr int kItemsPerSm = 4, kSms = kMaxCtas;
     FullCut c;
     c.half_tokens = kRows / s.R;
     c.unit_tokens = 2 * c.half_tokens;
     c.split = kSms * kItemsPerSm;
     c.min_tiles = s.paged ? 2 : 4;
     const int64_t units = std::max<int64_t>(1, (s.tokens + c.unit_tokens - 1) / c.unit_tokens) * s.Hkv;
+    const int64_t keys = s.paged ? (int64_t)s.max_pages * s.page_size : s.key_tokens;
+    c.fold_floats = keys > kFoldHalves * kHalf ? (size_t)kMaxCtas * 2 * kRows * (s.d + 4) : 0;
     c.max_parts = (int)std::min<int64_t>(kMaxParts, std::max<int64_t>(1, (4 * kSms + units - 1) / units));
     return c;
 }
@@ -910,7 +984,7 @@ FullCut full_tc_cut(const FullShape &s) {
 cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut &c,
                            const FullPlan *plan, const FullSeq *seqs, const void *Q,
                            const void *K, const void *V, void *O, float *lse, float *part_o,
-                           float *part_lse, uint32_t *err, cudaStream_t st) {
+                           float *part_lse, float *fold, uint32_t *err, cudaStream_t st) {
     TcArgs a;
     a.s = s; a.q = q; a.c = c;
     a.plan = plan; a.seqs = seqs;
@@ -923,6 +997,7 @@ cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut 
     a.wide = ((uintptr_t)O & 31u) == 0;
     a.scale_log2 = s.scale * kLog2e;
     a.lag = kMaxLag / a.scale_log2;
+    a.fold = fold;
     a.box = kFullKeys;                   // the largest power of two that divides pages and tiles
     if (s.paged)
         while (s.page_size % a.box != 0) a.box /= 2;

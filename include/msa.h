@@ -535,7 +535,9 @@ MSA_EXPORT size_t msa_attn_workspace_size(const msa_attn_params_t *params, int p
  * 0 (a score of -infinity, or too far under the row's largest for fp32) times
  * an infinite value is NaN.  A query whose every score is -infinity gets O = 0
  * and lse = -infinity.  bf16: fp32 scores, softmax and sums; the weights are
- * rounded to bf16 for the product with V.
+ * rounded to bf16 for the product with V.  The tensor cores' fp32 sums are cut
+ * off towards 0, which takes up to 0.2 % off O (0.04 % measured): no more than
+ * 65536 keys enter one at a time, so that this does not grow with the length.
  *
  * Q [tokens, Hq, d], K, V [key_tokens, Hkv, d] (dtype, read); cu_seqlens_q,
  * cu_seqlens_k [B + 1] int32 (device, read; the same array for plain

@@ -1,0 +1,98 @@
+"""Full causal attention over key runs so long that the order and the rounding of the sums count.
+
+A call of 2400 tokens of 64 heads over one KV head has more units than the GPU has room for, so
+that no row's keys are cut into runs: every row's sums are one run (the workspace then has no
+partial results).  Caches of a few pages, read again and again, stand for long contexts."""
+import math
+
+import pytest
+import torch
+
+from tests import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+T, PAGE, HEADS = 2400, 256, 64
+
+
+def _msa():
+    import block_sparse_long_03_b200 as msa
+    return msa
+
+
+def _expect(q, K, V, counts):
+    """(O, lse, bound of O, of lse) in 64 bits of one token's heads q [Hq, d] over keys K, V [n, d]
+    that occur counts [n] times each.
+
+    Scores, weights and their rounding as in serving_ref.attention: A (2 e + 2^-18 + 2^-8) for the
+    scores, exp and the weights' rounding to bf16 (none where all weights are powers of two), u |O|
+    for O's.  Sums: at most 2^16 keys go through the tensor core's fp32 sums at once, four keys an
+    addition, each cut off by less than 2^-23 of the sum: 2^14 2^-23 = 2^-9.  The row sum adds 64
+    keys at a time, 2^10 of those and then runs of 2^16 keys, each rounded by 2^-24; 64 keys take
+    32 + 1 additions: (2^10 + 2^6 + 33) 2^-24 < 2^-13, for the lse too."""
+    d = q.shape[1]
+    q, K, V, counts = q.double(), K.double(), V.double(), counts.double()
+    s = q @ K.T / math.sqrt(d)
+    e = float(((d + 8) * 2.0 ** -23 * (q.abs() @ K.abs().T) / math.sqrt(d)).max())
+    lse = torch.logsumexp(s + counts.log(), 1)
+    w = counts * torch.exp(s - lse[:, None])
+    O, A = w @ V, w @ V.abs()
+    r = 2.0 ** -8 if bool((s != 0).any()) else 0.0
+    bound = A * (2 * e + 2.0 ** -18 + r + 2.0 ** -9 + 2.0 ** -13) + ref.U[BF16] * O.abs()
+    return O, lse, bound, e + 2.0 ** -18 + 2.0 ** -13 + 2.0 ** -22 * lse.abs()
+
+
+def _assert(O, lse, want, where):
+    Or, lr, Ob, lb = want
+    over = (O.double() - Or).abs() - Ob
+    assert bool((over <= 0).all()), \
+        f"{where}: O off by {float(over.max())} over the bound {float(Ob.flatten()[over.argmax()])}"
+    assert bool(((lse.double() - lr).abs() <= lb).all()), where
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scores", [False, True])
+def test_a_long_run_keeps_its_sum(d, scores):
+    """A single token over 2^22 keys, values with a mean of 1."""
+    msa, g = _msa(), torch.Generator().manual_seed(d)
+    L = 1 << 22
+    table = (torch.arange(L // PAGE, dtype=torch.int32) % 16).repeat(2, 1).cuda()
+    K = (torch.randn((16, PAGE, 1, d), generator=g) * scores).to(BF16).cuda()
+    V = (torch.rand((16, PAGE, 1, d), generator=g) + 0.5).to(BF16).cuda()
+    Q = torch.randn((T + 1, HEADS, d), generator=g).to(BF16).cuda()
+    lens = torch.tensor([T, L], dtype=torch.int32, device="cuda")
+    O, lse, ws = msa.attn_paged(Q, K, V, ref.offsets([T, 1]).cuda(), lens, table)
+    assert msa.msa_get_device_error(ws) == 0
+    counts = torch.full((16 * PAGE,), L / (16 * PAGE), device="cuda")
+    _assert(O[T], lse[T], _expect(Q[T], K.view(-1, d), V.view(-1, d), counts), "long run")
+    counts = torch.ones(T, device="cuda")                 # the prompt's last token
+    _assert(O[T - 1], lse[T - 1],
+            _expect(Q[T - 1], K.view(-1, d)[:T], V.view(-1, d)[:T], counts), "prompt")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_chunk_whose_maximum_moves_late(d):
+    """A chunk of 2400 tokens at the end of 200,001 keys whose scores rise at keys around 66,000,
+    140,000 and 199,700: the running maximum moves in the first half behind a moved sum, between
+    two and near the end, where only the last tokens see the keys."""
+    msa, g = _msa(), torch.Generator().manual_seed(d + 1)
+    L = 200001
+    n = -(-L // PAGE)
+    table = (torch.arange(n, dtype=torch.int32) % 16).view(1, n)
+    K = torch.randn((19, PAGE, 1, d), generator=g).to(BF16)
+    V = (torch.randn((19, PAGE, 1, d), generator=g) + 0.5).to(BF16)
+    for i, key in enumerate((65536 + 10, 140000, 199700)):
+        table[0, key // PAGE] = 16 + i
+        K[16 + i] *= 4 + 4 * i
+    K, V, table = K.cuda(), V.cuda(), table.cuda()
+    Q = torch.randn((T, HEADS, d), generator=g).to(BF16).cuda()
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    O, lse, ws = msa.attn_paged(Q, K, V, ref.offsets([T]).cuda(), lens, table)
+    assert msa.msa_get_device_error(ws) == 0
+    rows = table[0].long()
+    Kf, Vf = K[rows].view(-1, d)[:L], V[rows].view(-1, d)[:L]
+    for t in (0, 1, 1999, 2090, 2098, 2099, 2100, 2101, 2300, T - 1):
+        seen = L - T + t + 1
+        _assert(O[t], lse[t], _expect(Q[t], Kf[:seen], Vf[:seen], torch.ones(seen, device="cuda")),
+                f"token {t}")
