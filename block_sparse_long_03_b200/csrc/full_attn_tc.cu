@@ -83,6 +83,7 @@ struct TcArgs {
     int box;                             // key rows of one TMA box
     bool wide;                           // O is 32-byte aligned
     float scale_log2, lag;               // lag: kMaxLag in units of raw scores
+    uint64_t run_ns;                     // limit of a wait that may last as long as a key run
 };
 
 // A work item as the loading warp hands it to the others.
@@ -464,7 +465,8 @@ __device__ void check_role(const TcArgs &a, Bars *bar, uint8_t *sKV) {
     uint32_t edge_phase = 0;                             // per slot
     for (int k = 0;; ++k) {
         const int slot = k & 1;
-        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort)) return;
+        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort, a.run_ns))
+            return;
         const Item w = bar->item[slot];
         if (w.valid) {
             const int limit = w.pos0 + w.nt;
@@ -476,7 +478,7 @@ __device__ void check_role(const TcArgs &a, Bars *bar, uint8_t *sKV) {
                 const int t = stream_a(w, s) + j;
                 if (edge_tile(w, t)) {
                     if (!tc::mbar_wait(&bar->issued[ring.slot], (edge_phase >> ring.slot) & 1,
-                                       a.err, &bar->abort))
+                                       a.err, &bar->abort, a.run_ns))
                         return false;
                     edge_phase ^= 1u << ring.slot;
                     if (!tc::mbar_wait(&bar->full[ring.slot], ring.phase, a.err, &bar->abort))
@@ -695,7 +697,8 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     for (int k = 0;; ++k) {
         const int slot = k & 1;
-        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort)) return;
+        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort, a.run_ns))
+            return;
         const Item &w = bar->item[slot];                 // read where needed: registers are short
         if (!w.valid) return;
         const int first_tok = w.pair ? s * a.c.half_tokens : 0;
@@ -998,6 +1001,10 @@ cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut 
     a.scale_log2 = s.scale * kLog2e;
     a.lag = kMaxLag / a.scale_log2;
     a.fold = fold;
+    // A stream without keys and the value check sit an item out: its key run
+    // can be the whole capacity.  A tile takes 1 to 3 us; 20 are allowed.
+    const int64_t keys = s.paged ? (int64_t)s.max_pages * s.page_size : s.key_tokens;
+    a.run_ns = tc::kWaitLimitNs + (uint64_t)(keys / kFullKeys) * 20000;
     a.box = kFullKeys;                   // the largest power of two that divides pages and tiles
     if (s.paged)
         while (s.page_size % a.box != 0) a.box /= 2;

@@ -96,3 +96,26 @@ def test_a_chunk_whose_maximum_moves_late(d):
         seen = L - T + t + 1
         _assert(O[t], lse[t], _expect(Q[t], Kf[:seen], Vf[:seen], torch.ones(seen, device="cuda")),
                 f"token {t}")
+
+
+def test_a_key_run_of_seconds():
+    """A single token over 2^29 keys (on 16 pages, again and again) beside 2400 prompt tokens, which
+    leave it one key run and one stream: 4 million tiles one after another, about 5 s, longer than the
+    2 s that a wait on another role's next step may take.  The stream without keys and the check
+    of the values wait that long for their turn, and nothing may give up.  All scores are 0 and
+    the values constant: the sums of weights are exact in fp32 (multiples of 64 up to 2^29), those of
+    equal values too, so that O is the value."""
+    msa, page, d, Hq = _msa(), 256, 64, 64
+    L, T = 1 << 29, 2400
+    table = (torch.arange(L // page, dtype=torch.int32, device="cuda") % 16).repeat(2, 1)
+    value = (2.0 ** -(torch.arange(d) % 3)).to(BF16).cuda()
+    Kc = torch.zeros((16, page, 1, d), dtype=BF16, device="cuda")
+    Vc = value.expand(16, page, 1, d).contiguous()
+    Q = torch.ones((T + 1, Hq, d), dtype=BF16, device="cuda")
+    lens = torch.tensor([T, L], dtype=torch.int32, device="cuda")
+    O, lse, ws = msa.attn_paged(Q, Kc, Vc, ref.offsets([T, 1]).cuda(), lens, table)
+    assert ws.numel() < 11 << 20                       # no partial results (two a row: 157 MB)
+    assert msa.msa_get_device_error(ws) == 0
+    assert torch.equal(O, value.expand_as(O))
+    want = torch.log(torch.cat([torch.arange(1, T + 1), torch.tensor([L])]).double())
+    assert float((lse.cpu().double() - want[:, None]).abs().max()) <= 2.0 ** -22 * math.log(L)
