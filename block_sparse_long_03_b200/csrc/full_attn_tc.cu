@@ -604,40 +604,55 @@ __device__ __forceinline__ float weights(const uint32_t (&v)[kHalf], uint32_t tP
     return x + y;
 }
 
-// Infinities and NaN among the values of keys lo .. hi, which the products left
-// out, enter one row's stored result (`out`, floats or bf16) with the weights
-// of their keys, worked out again against the running maximum m: a weight of
-// 0 (a score of -infinity, or far below m) gives NaN, as in a product.  Apart
-// from the epilogue's loop, and on its stores, so that the loop keeps its
-// registers.  Returns whether the row got a NaN.
+// What is left of a stored row (`out`, floats or bf16) where `odd` (its item has
+// infinities or NaN that the products left out) or its weights are all 0.
+// The infinities and NaN among the values of keys lo .. hi enter with the weights
+// of their keys, worked out again against the running maximum m: a weight of 0 (a
+// score of -infinity, or far below m) gives NaN, as in a product.  Returns whether
+// the row has a NaN.  Apart from the epilogue's loop, and on what it stored, so
+// that the loop stays small.
 template <int D, bool kPaged, typename T>
-__device__ __noinline__ bool add_odd(const TcArgs &a, int b, int g, int64_t q_row, int head, int k0,
-                                     int lo, int hi, float m, T *out) {
-    const __nv_bfloat16 *q = a.Q + q_row * a.s.q_stride + (int64_t)(g * a.s.R + head) * D;
-    bool nan = false;
-    for (int j = lo; j <= hi; ++j) {
-        int64_t row = (int64_t)k0 + j;
+__device__ __forceinline__ bool finish_row(const TcArgs &a, const Item &w, bool odd, int64_t q_row,
+                                           int head, int lo, int hi, float m, T *out) {
+    const __nv_bfloat16 *q = a.Q + q_row * a.s.q_stride + (int64_t)(w.g * a.s.R + head) * D;
+    for (int j = lo; odd && j <= hi; ++j) {
+        int64_t row = (int64_t)w.k0 + j;
         if (kPaged)
-            row = (int64_t)a.q.block_table[(int64_t)b * a.s.max_pages + j / a.s.page_size] *
+            row = (int64_t)a.q.block_table[(int64_t)w.b * a.s.max_pages + j / a.s.page_size] *
                       a.s.page_size + j % a.s.page_size;
-        const __nv_bfloat16 *v = a.V + row * a.s.v_stride + (int64_t)g * D;
+        const __nv_bfloat16 *v = a.V + row * a.s.v_stride + (int64_t)w.g * D;
         float p = -1.f;                                  // not worked out yet
+#pragma unroll 1
         for (int c = 0; c < D; ++c) {
             const float f = __bfloat162float(v[c]);
             if (isfinite(f)) continue;
             if (p == -1.f) {
-                const __nv_bfloat16 *k = a.K + row * a.s.k_stride + (int64_t)g * D;
+                const __nv_bfloat16 *k = a.K + row * a.s.k_stride + (int64_t)w.g * D;
                 float dot = 0.f;
+#pragma unroll 4
                 for (int e = 0; e < D; ++e)
                     dot = fmaf(__bfloat162float(q[e]), __bfloat162float(k[e]), dot);
                 p = tc::ex2_approx(fmaf(dot, a.scale_log2, m == -INFINITY ? 0.f : -m * a.scale_log2));
             }
-            const float x = fmaf(p, f, to_f32<T>(out[c]));
-            nan |= x != x;
-            out[c] = from_f32<T>(x);
+            out[c] = from_f32<T>(fmaf(p, f, to_f32<T>(out[c])));
         }
     }
+    bool nan = false;
+#pragma unroll 4
+    for (int c = 0; c < D; ++c) nan |= to_f32<T>(out[c]) != to_f32<T>(out[c]);
     return nan;
+}
+template <int D, bool kPaged>
+__device__ __noinline__ bool finish_row(const TcArgs &a, const Item &w, bool odd, int stream, int tok,
+                                        int head, int64_t part, float m) {
+    const int t = (w.pair ? stream * a.c.half_tokens : 0) + tok, t0 = stream_a(w, stream);
+    const int lo = max(t0 * kFullKeys, w.pos0 + 1);
+    const int hi = min(w.pos0 + t, (t0 + stream_n(w, stream)) * kFullKeys - 1);
+    const int64_t q_row = w.q0 + t;
+    if (w.parts > 0)
+        return finish_row<D, kPaged>(a, w, odd, q_row, head, lo, hi, m, a.part_o + part * D);
+    return finish_row<D, kPaged>(a, w, odd, q_row, head, lo, hi, m,
+                                 a.O + (q_row * a.s.Hq + w.g * a.s.R + head) * D);
 }
 
 // The earlier sums of a row of this CTA's stream s.
@@ -806,10 +821,6 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                     float x[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) x[i] = zero ? 0.f : __uint_as_float(o[i]) * inv;
-                    if (l == 0.f) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) nan |= x[i] != x[i];
-                    }
                     if (valid && w.parts > 0) {
                         float *dst = a.part_o + part * D + c;
 #pragma unroll
@@ -829,15 +840,8 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                     }
                 }
             }
-            if (odd && valid && !zero) {
-                const int lo = max(t0 * kFullKeys, w.pos0 + 1);
-                const int hi = min(first_pos + tok, (t0 + n) * kFullKeys - 1);
-                const int64_t q_row = w.q0 + first_tok + tok;
-                nan |= w.parts > 0 ? add_odd<D, kPaged>(a, w.b, w.g, q_row, head, w.k0, lo, hi, m,
-                                                        a.part_o + part * D)
-                                   : add_odd<D, kPaged>(a, w.b, w.g, q_row, head, w.k0, lo, hi, m,
-                                                        a.O + at * D);
-            }
+            if (valid && !zero && (odd || l == 0.f))
+                nan = finish_row<D, kPaged>(a, w, odd, s, tok, head, part, m);
             if (valid) {
                 const float out_lse = l != 0.f ? m * a.s.scale + logf(l)
                                                : nan ? kNanPart : -INFINITY;
