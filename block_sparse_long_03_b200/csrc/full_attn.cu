@@ -432,15 +432,20 @@ full_simt_kernel(FullShape s, FullSeqs sq, FullCut c, const FullPlan *plan, cons
                 if (tid % 2 == 0) alpha[tid / 2] = a;
             }
             __syncthreads();
+            // The tile's weighted values are summed by themselves and then added:
+            // one value after another onto the sum of 2^18 equal ones is 0.26 %
+            // off, this way 0.002 to 0.005 %.
+            float t[4][D / 8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = alpha[4 * y + i];
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int k = 0; k < D / 8; ++k) acc[i][k] *= a;
-            }
+                for (int k = 0; k < D / 8; ++k) t[i][k] = 0.f;
             // a tile that some row sees only in part: that row leaves the
             // later values out (they may be infinite or NaN)
             const bool whole = j0 + kSimtKeys <= pos0 + 1;
+            // (unrolled whole the loop spills at D = 128: 2.1 ms for 512 tokens of 32
+            // heads over 4096 keys, by eight 1.62)
+#pragma unroll 8
             for (int j = 0; j < kSimtKeys; ++j) {
                 float4 v[D / 32];
 #pragma unroll
@@ -451,12 +456,18 @@ full_simt_kernel(FullShape s, FullSeqs sq, FullCut c, const FullPlan *plan, cons
                     const float w = ps[(4 * y + i) * 36 + j];
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {
-                        acc[i][4 * k] = fmaf(w, v[k].x, acc[i][4 * k]);
-                        acc[i][4 * k + 1] = fmaf(w, v[k].y, acc[i][4 * k + 1]);
-                        acc[i][4 * k + 2] = fmaf(w, v[k].z, acc[i][4 * k + 2]);
-                        acc[i][4 * k + 3] = fmaf(w, v[k].w, acc[i][4 * k + 3]);
+                        t[i][4 * k] = fmaf(w, v[k].x, t[i][4 * k]);
+                        t[i][4 * k + 1] = fmaf(w, v[k].y, t[i][4 * k + 1]);
+                        t[i][4 * k + 2] = fmaf(w, v[k].z, t[i][4 * k + 2]);
+                        t[i][4 * k + 3] = fmaf(w, v[k].w, t[i][4 * k + 3]);
                     }
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = alpha[4 * y + i];
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) acc[i][k] = fmaf(acc[i][k], a, t[i][k]);
             }
         }
         if (tid % 2 == 0) {

@@ -119,3 +119,22 @@ def test_a_key_run_of_seconds():
     assert torch.equal(O, value.expand_as(O))
     want = torch.log(torch.cat([torch.arange(1, T + 1), torch.tensor([L])]).double())
     assert float((lse.cpu().double() - want[:, None]).abs().max()) <= 2.0 ** -22 * math.log(L)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp32_sums_of_equal_values(d):
+    """fp32, one token over 2^18 keys of equal values and scores: weights of 1 and an exact row sum.
+    The values of 32 keys are summed (31 roundings of at most 2^-24 of the sum), and 2^13 such sums
+    are added (one each); the quotient rounds twice more."""
+    msa, page, L = _msa(), 64, 1 << 18
+    table = (torch.arange(L // page, dtype=torch.int32, device="cuda") % 4).view(1, -1)
+    value = torch.linspace(0.55, 1.45, d, device="cuda")
+    K = torch.zeros((4, page, 1, d), device="cuda")
+    V = value.expand(4, page, 1, d).contiguous()
+    O, lse, ws = msa.attn_paged(torch.ones((1, 2, d), device="cuda"), K, V,
+                                ref.offsets([1]).cuda(), torch.tensor([L], dtype=torch.int32).cuda(),
+                                table)
+    assert msa.msa_get_device_error(ws) == 0
+    off = (O.double() / value.double() - 1).abs()
+    assert float(off.max()) <= (31 + 2 ** 13 + 2) * 2.0 ** -24, float(off.max())
+    assert float((lse.double() - math.log(L)).abs().max()) <= 2.0 ** -22 * math.log(L)
