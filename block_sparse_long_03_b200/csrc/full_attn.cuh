@@ -52,7 +52,7 @@ constexpr int kMaxParts = 64;            // key runs of a unit, at most (twice a
 // max_parts runs a unit.
 struct FullCut {
     int unit_tokens, half_tokens, split, max_parts, min_tiles;
-    size_t fold_floats;                  // workspace for the sums of long key runs
+    size_t carry_floats;                  // workspace for the sums carried along key runs
 };
 
 // Key runs that the partial results of a row of sequence s are kept for: 0
@@ -90,7 +90,7 @@ FullCut full_tc_cut(const FullShape &s);
 cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut &c,
                            const FullPlan *plan, const FullSeq *seqs, const void *Q,
                            const void *K, const void *V, void *O, float *lse, float *part_o,
-                           float *part_lse, float *fold, uint32_t *err, cudaStream_t st);
+                           float *part_lse, float *carry, uint32_t *err, cudaStream_t st);
 
 // The call's kernels follow one another closely (programmatic dependent
 // launch): the next one may be set up as soon as every block of this one has

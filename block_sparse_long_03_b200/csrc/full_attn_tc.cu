@@ -56,12 +56,15 @@ constexpr float kMaxLag = 8.f;           // log2 of how far P may pass 1
 constexpr int kHalf = 64;                // keys of one S / P buffer
 constexpr int kMaxCtas = 148;            // SMs of a B200
 
-// Halves whose products are summed in TMEM before O and the row sum move to
-// fp32 sums in memory.  The tensor core adds to its fp32 sums four keys at a time
-// and cuts the result off, towards 0: over 2^20 keys at once O came out 0.66 %
-// too small, over 2^22 2.6 %, over 2^26 a third; over 2^16, this many, 0.04 %,
-// a tenth of bf16's rounding.
-constexpr int kFoldHalves = 1024;
+// Halves whose products are summed in TMEM at most: an item of longer key runs
+// is handed out in pieces, each one's sums carried to the next in memory.  The
+// tensor core adds to its fp32 sums four keys at a time and cuts the result off,
+// towards 0: over 2^20 keys at once O came out 0.66 % too small, over 2^22 2.6 %,
+// over 2^26 a third; over 2^16, this many, 0.04 %, a tenth of bf16's rounding.
+// (Carried inside the loop over the halves instead, the loop's registers made
+// every call of short sequences 2 to 4 % slower.)
+constexpr int kPieceHalves = 1024;
+constexpr int kCarryIn = 1, kCarryOut = 2;   // Item::carry: pieces before this one, behind it
 
 template <int D> constexpr int ring_slots() { return D == 128 ? 5 : 10; }
 template <int D> constexpr size_t tc_smem() {
@@ -78,12 +81,11 @@ struct TcArgs {
     const __nv_bfloat16 *Q, *K, *V;      // Q, K: read for infinite values' weights only
     __nv_bfloat16 *O;
     float *lse, *part_o, *part_lse;
-    float *fold;                         // [CTA][stream][row][d + 4]: earlier sums of O, of weights
+    float *carry;                        // [CTA][stream][row][d + 8]: earlier pieces' sums
     uint32_t *err;
     int box;                             // key rows of one TMA box
     bool wide;                           // O is 32-byte aligned
     float scale_log2, lag;               // lag: kMaxLag in units of raw scores
-    uint64_t run_ns;                     // limit of a wait that may last as long as a key run
 };
 
 // A work item as the loading warp hands it to the others.
@@ -91,7 +93,7 @@ struct Item {
     int valid, b, g, q0;                 // q0: row of Q of the unit's first token
     int nt, pos0, k0, pair;              // tokens; position of the first; packed key row 0
     int a0, a1, h0, h1;                  // each stream's first key tile and number of halves
-    int part, parts, pad0, pad1;         // key run, and how many the rows' results come in
+    int part, parts, carry, pad;         // key run, and how many the rows' results come in
 };
 
 __device__ __forceinline__ int stream_a(const Item &w, int s) { return s ? w.a1 : w.a0; }
@@ -120,6 +122,7 @@ __device__ __forceinline__ Item make_item(const TcArgs &a, const FullSeq &q, int
     w.k0 = q.k0;
     w.pair = w.nt > a.c.half_tokens;
     w.parts = full_row_parts(q, a.c, t0);
+    w.carry = 0;
     const int lo = w.part * q.tiles;
     auto run = [&](int tokens) {         // halves of this part that the first tokens see
         const int seen = (max(0, w.pos0 + tokens) + kHalf - 1) / kHalf;
@@ -215,20 +218,34 @@ __device__ void load_role(const TcArgs &a, Bars *bar, uint8_t *sQ, uint8_t *sKV,
     const int items = a.plan->items;
     const uint32_t q_tile_bytes = (uint32_t)(a.c.half_tokens * a.s.R) * 128 * kAtoms;
     Ring ring;
-    int b = 0, q_uses = 0;
+    int b = 0, q_uses = 0, left0 = 0, left1 = 0;         // the streams' halves from this piece on
     bool ok = true;
+    Item w{};
     for (int k = 0;; ++k) {
-        int item = blockIdx.x;
-        if (k > 0) {
-            if (lane == 0) item = gridDim.x + atomicAdd(a.next, 1);
-            item = __shfl_sync(0xffffffffu, item, 0);
-        }
         const int slot = k & 1;
-        Item w{};
-        if (item < items) {
-            b = full_find_seq(a.seqs, a.s.B, b, item, lane);
-            w = make_item(a, a.seqs[b], b, item);
+        if (w.carry & kCarryOut) {
+            w.a0 += kPieceHalves / 2;
+            w.a1 += kPieceHalves / 2;
+            left0 -= w.h0;
+            left1 -= w.h1;
+            w.carry = kCarryIn;
+        } else {
+            int item = blockIdx.x;
+            if (k > 0) {
+                if (lane == 0) item = gridDim.x + atomicAdd(a.next, 1);
+                item = __shfl_sync(0xffffffffu, item, 0);
+            }
+            w = Item{};
+            if (item < items) {
+                b = full_find_seq(a.seqs, a.s.B, b, item, lane);
+                w = make_item(a, a.seqs[b], b, item);
+            }
+            left0 = w.h0;
+            left1 = w.h1;
         }
+        w.h0 = min(left0, kPieceHalves);
+        w.h1 = min(left1, kPieceHalves);
+        if (max(left0, left1) > kPieceHalves) w.carry |= kCarryOut;
         const int limit = w.pos0 + w.nt;                 // no row attends key `limit` or later
         // paged: this lane's box, the cache row of each stream's tile, and of
         // its next one (whose page id is on its way meanwhile)
@@ -397,7 +414,7 @@ __device__ void mma_role(const TcArgs &a, Bars *bar, uint32_t tmem, uint32_t sQ,
 #pragma unroll
             for (int c = 0; c < kHalf / 16; ++c)
                 tc::mma_ts(tO, tS + b * kHalf + c * 8, desc(va + (b * 4 + c) * 128), idesc_o,
-                           (i % kFoldHalves > 0 || c > 0) ? 1u : 0u);
+                           (i > 0 || c > 0) ? 1u : 0u);
             if (i + 2 == h) tc::mma_commit(&bar->o_prev[me]);
             if (i + 1 == h) tc::mma_commit(&bar->o_full[me]);
             return true;
@@ -465,8 +482,7 @@ __device__ void check_role(const TcArgs &a, Bars *bar, uint8_t *sKV) {
     uint32_t edge_phase = 0;                             // per slot
     for (int k = 0;; ++k) {
         const int slot = k & 1;
-        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort, a.run_ns))
-            return;
+        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort)) return;
         const Item w = bar->item[slot];
         if (w.valid) {
             const int limit = w.pos0 + w.nt;
@@ -478,7 +494,7 @@ __device__ void check_role(const TcArgs &a, Bars *bar, uint8_t *sKV) {
                 const int t = stream_a(w, s) + j;
                 if (edge_tile(w, t)) {
                     if (!tc::mbar_wait(&bar->issued[ring.slot], (edge_phase >> ring.slot) & 1,
-                                       a.err, &bar->abort, a.run_ns))
+                                       a.err, &bar->abort))
                         return false;
                     edge_phase ^= 1u << ring.slot;
                     if (!tc::mbar_wait(&bar->full[ring.slot], ring.phase, a.err, &bar->abort))
@@ -604,7 +620,14 @@ __device__ __forceinline__ float weights(const uint32_t (&v)[kHalf], uint32_t tP
     return x + y;
 }
 
-// What is left of a stored row (`out`, floats or bf16) where `odd` (its item has
+// The sums of the pieces so far of a row of this CTA's stream s: O (not yet
+// divided), the maximum it is taken against, the weights.
+template <int D>
+__device__ __forceinline__ float *carried_row(const TcArgs &a, int s, int row) {
+    return a.carry + ((blockIdx.x * 2 + s) * (int64_t)kRows + row) * (D + 8);
+}
+
+// What is left of a stored row (`out`: carried on, a partial result or O) where `odd` (its item has
 // infinities or NaN that the products left out) or its weights are all 0.
 // The infinities and NaN among the values of keys lo .. hi enter with the weights
 // of their keys, worked out again against the running maximum m: a weight of 0 (a
@@ -649,56 +672,13 @@ __device__ __noinline__ bool finish_row(const TcArgs &a, const Item &w, bool odd
     const int lo = max(t0 * kFullKeys, w.pos0 + 1);
     const int hi = min(w.pos0 + t, (t0 + stream_n(w, stream)) * kFullKeys - 1);
     const int64_t q_row = w.q0 + t;
-    if (w.parts > 0)
-        return finish_row<D, kPaged>(a, w, odd, q_row, head, lo, hi, m, a.part_o + part * D);
+    if (w.parts > 0 || (w.carry & kCarryOut))
+        return finish_row<D, kPaged>(a, w, odd, q_row, head, lo, hi, m,
+                                     w.carry & kCarryOut
+                                         ? carried_row<D>(a, stream, tok * a.s.R + head)
+                                         : a.part_o + part * D);
     return finish_row<D, kPaged>(a, w, odd, q_row, head, lo, hi, m,
                                  a.O + (q_row * a.s.Hq + w.g * a.s.R + head) * D);
-}
-
-// The earlier sums of a row of this CTA's stream s.
-template <int D>
-__device__ __forceinline__ float *fold_sums(const TcArgs &a, int s, int row) {
-    return a.fold + ((blockIdx.x * 2 + s) * (int64_t)kRows + row) * (D + 4);
-}
-// O and the sum of weights l so far join the row's earlier sums (none yet where
-// `first`).
-template <int D>
-__device__ __noinline__ void fold_in(uint32_t tO, float *sums, float l, bool first) {
-#pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        __syncwarp();
-        tc::tmem_ld32(tO + c, o);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            float4 *at = (float4 *)(sums + c + i);
-            float4 v = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *at;
-            v.x += __uint_as_float(o[i]);
-            v.y += __uint_as_float(o[i + 1]);
-            v.z += __uint_as_float(o[i + 2]);
-            v.w += __uint_as_float(o[i + 3]);
-            *at = v;
-        }
-    }
-    sums[D] = (first ? 0.f : sums[D]) + l;
-}
-// The earlier sums join O; returns their sum of weights.
-template <int D>
-__device__ __noinline__ float fold_out(uint32_t tO, const float *sums) {
-#pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        __syncwarp();
-        tc::tmem_ld32(tO + c, o);
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            o[i] = __float_as_uint(__uint_as_float(o[i]) + sums[c + i]);
-        tc::tmem_st32(tO + c, o);
-    }
-    tc::tmem_st_wait();
-    return sums[D];
 }
 
 template <int D, bool kPaged>
@@ -712,8 +692,7 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     for (int k = 0;; ++k) {
         const int slot = k & 1;
-        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort, a.run_ns))
-            return;
+        if (!tc::mbar_wait(&bar->item_full[slot], (k >> 1) & 1, a.err, &bar->abort)) return;
         const Item &w = bar->item[slot];                 // read where needed: registers are short
         if (!w.valid) return;
         const int first_tok = w.pair ? s * a.c.half_tokens : 0;
@@ -723,75 +702,59 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
         const int first_pos = w.pos0 + first_tok;        // of the stream's first token
         const int t0 = stream_a(w, s), h = stream_h(w, s), n = (h + 1) / 2;
         float m = -INFINITY, l = 0.f;
-        // P V of halves i - 1 and before is in O once S(i + 1), issued after it,
-        // is complete; at the last half o_prev tells
-        auto products_done = [&](int i) {
-            const int b = (i + 1) & 1;
-            return i + 1 < h ? tc::mbar_wait(&bar->s_full[s][b], (s_phase >> b) & 1, a.err, &bar->abort)
-                             : tc::mbar_wait(&bar->o_prev[s], prev_phase, a.err, &bar->abort);
-        };
-        for (int i0 = 0; i0 < h; i0 += kFoldHalves) {
-            const int end = min(h, i0 + kFoldHalves);
-            if (i0 > 0 && busy) {                        // the next product starts O anew
-                if (!products_done(i0)) return;
+        for (int i = 0; i < h; ++i) {
+            const int b = i & 1;
+            const uint32_t tB = tS + b * kHalf;
+            if (!tc::mbar_wait(&bar->s_full[s][b], (s_phase >> b) & 1, a.err, &bar->abort)) return;
+            s_phase ^= 1u << b;
+            if (busy) {
                 tc::tc_fence_after();
-                fold_in<D>(tO, fold_sums<D>(a, s, row), l, i0 == kFoldHalves);
-                l = 0.f;
-            }
-            for (int i = i0; i < end; ++i) {
-                const int b = i & 1;
-                const uint32_t tB = tS + b * kHalf;
-                if (!tc::mbar_wait(&bar->s_full[s][b], (s_phase >> b) & 1, a.err, &bar->abort)) return;
-                s_phase ^= 1u << b;
-                if (busy) {
-                    tc::tc_fence_after();
-                    uint32_t v[kHalf];
-                    tc::tmem_ld32(tB, *(uint32_t(*)[32])v);
-                    tc::tmem_ld32(tB + 32, *(uint32_t(*)[32])(v + 32));
-                    tc::tmem_ld_wait();
-                    const int key0 = t0 * kFullKeys + i * kHalf;
-                    const bool edge = key0 + kHalf > first_pos + 1;
-                    if (edge) {
-                        const int lim = first_pos + tok - key0;   // columns above lim are not attended
+                uint32_t v[kHalf];
+                tc::tmem_ld32(tB, *(uint32_t(*)[32])v);
+                tc::tmem_ld32(tB + 32, *(uint32_t(*)[32])(v + 32));
+                tc::tmem_ld_wait();
+                const int key0 = t0 * kFullKeys + i * kHalf;
+                const bool edge = key0 + kHalf > first_pos + 1;
+                if (edge) {
+                    const int lim = first_pos + tok - key0;   // columns above lim are not attended
 #pragma unroll
-                        for (int c = 0; c < kHalf; ++c)
-                            if (c > lim) v[c] = __float_as_uint(-INFINITY);
-                    }
-                    const float top = row_max(v);
-                    const bool move = valid && !(top <= m + a.lag);   // (a NaN moves m too)
-                    if (i == 0) {
-                        m = top;
-                    } else if (__any_sync(0xffffffffu, move)) {
-                        // O is rescaled between the products of halves i - 1 and i
-                        if (!products_done(i)) return;
-                        tc::tc_fence_after();
-                        const float f = move ? tc::ex2_approx((m - top) * a.scale_log2) : 1.f;
-                        if (move) m = top;
-                        l *= f;
-                        if (i0 > 0) {
-                            float *x = fold_sums<D>(a, s, row);
-#pragma unroll 1
-                            for (int c = 0; c <= D; ++c) x[c] *= f;
-                        }
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tc::tmem_ld32(tO + c, o);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc::tmem_st32(tO + c, o);
-                        }
-                    }
-                    const float mb = m == -INFINITY ? 0.f : -m * a.scale_log2;
-                    l += weights(v, tB, scale2, pack2(mb, mb));
-                    tc::tmem_st_wait();
-                    tc::tc_fence_before();
+                    for (int c = 0; c < kHalf; ++c)
+                        if (c > lim) v[c] = __float_as_uint(-INFINITY);
                 }
-                __syncwarp();
-                arrive_if(lane == 0, &bar->p_full[s][b]);
+                const float top = row_max(v);
+                const bool move = valid && !(top <= m + a.lag);   // (a NaN moves m too)
+                if (i == 0) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, move)) {
+                    // O is rescaled between the products of halves i - 1 and
+                    // i.  The first is complete once S(i + 1), issued after
+                    // it, is; at the last half o_prev tells.
+                    if (i + 1 < h ? !tc::mbar_wait(&bar->s_full[s][b ^ 1], (s_phase >> (b ^ 1)) & 1,
+                                                   a.err, &bar->abort)
+                                  : !tc::mbar_wait(&bar->o_prev[s], prev_phase, a.err, &bar->abort))
+                        return;
+                    tc::tc_fence_after();
+                    const float f = move ? tc::ex2_approx((m - top) * a.scale_log2) : 1.f;
+                    if (move) m = top;
+                    l *= f;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(tO + c, o);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc::tmem_st32(tO + c, o);
+                    }
+                }
+                const float mb = m == -INFINITY ? 0.f : -m * a.scale_log2;
+                l += weights(v, tB, scale2, pack2(mb, mb));
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
             }
+            __syncwarp();
+            arrive_if(lane == 0, &bar->p_full[s][b]);
         }
         // epilogue: O / l and the log-sum-exp, final or as one of the row's parts
         if (h > 0) {
@@ -801,15 +764,26 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
         }
         if (h > 1) prev_phase ^= 1;
         if (busy && (w.pair || s == 0 || a.c.max_parts > 1)) {
-            if (h > kFoldHalves) l += fold_out<D>(tO, fold_sums<D>(a, s, row));
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            float inv = 1.f, before = 0.f;               // factors of this O and of earlier pieces'
+            if (w.carry & kCarryIn) {
+                const float *y = carried_row<D>(a, s, row) + D;
+                const float top = y[0] != y[0] || y[0] > m ? y[0] : m;   // (NaN where one is)
+                if (top != -INFINITY) inv = tc::ex2_approx((m - top) * a.scale_log2);
+                before = top != -INFINITY ? tc::ex2_approx((y[0] - top) * a.scale_log2) : 1.f;
+                l = l * inv + y[1] * before;
+                m = top;
+            }
+            if (!(w.carry & kCarryOut)) {
+                const float r = l == 0.f ? 0.f : 1.f / l;
+                inv *= r;
+                before *= r;
+            }
             const int64_t at = (int64_t)(w.q0 + first_tok + tok) * a.s.Hq + w.g * a.s.R + head;
             const int64_t part = ((int64_t)w.part + (w.pair ? 0 : s)) * a.s.tokens * a.s.Hq + at;
             const bool odd = bar->odd[slot] == k + 1;
-            // no weights and nothing that a product with them could have made NaN
-            const bool zero = l == 0.f && (n == 0 || w.parts == 0);
-            bool nan = false;
-            if (n > 0 || w.parts == 0) {
+            const bool direct = w.parts == 0 && !(w.carry & kCarryOut);
+            const bool empty = direct && l == 0.f;       // O = 0
+            if (n > 0 || w.parts == 0 || w.carry) {
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
@@ -820,9 +794,16 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                     }
                     float x[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = zero ? 0.f : __uint_as_float(o[i]) * inv;
-                    if (valid && w.parts > 0) {
-                        float *dst = a.part_o + part * D + c;
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = empty || n == 0 ? 0.f : __uint_as_float(o[i]) * inv;
+                    if ((w.carry & kCarryIn) && !empty) {
+                        const float *y = carried_row<D>(a, s, row) + c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = fmaf(y[i], before, x[i]);
+                    }
+                    if (valid && !direct) {
+                        float *dst = w.carry & kCarryOut ? carried_row<D>(a, s, row) + c
+                                                         : a.part_o + part * D + c;
 #pragma unroll
                         for (int i = 0; i < 32; i += 8) store32(dst + i, (const uint32_t *)(x + i), true);
                     } else if (valid) {
@@ -840,13 +821,21 @@ __device__ void softmax_role(const TcArgs &a, Bars *bar, uint32_t tmem, int s) {
                     }
                 }
             }
-            if (valid && !zero && (odd || l == 0.f))
+            bool nan = false;
+            if (valid && !empty && (odd || l == 0.f) && (n > 0 || w.carry))
                 nan = finish_row<D, kPaged>(a, w, odd, s, tok, head, part, m);
             if (valid) {
                 const float out_lse = l != 0.f ? m * a.s.scale + logf(l)
                                                : nan ? kNanPart : -INFINITY;
-                if (w.parts > 0) a.part_lse[part] = out_lse;
-                else a.lse[at] = out_lse;
+                if (w.carry & kCarryOut) {
+                    float *y = carried_row<D>(a, s, row) + D;
+                    y[0] = m;
+                    y[1] = l;
+                } else if (w.parts > 0) {
+                    a.part_lse[part] = out_lse;
+                } else {
+                    a.lse[at] = out_lse;
+                }
             }
             tc::tc_fence_before();
         }
@@ -983,7 +972,7 @@ FullCut full_tc_cut(const FullShape &s) {
     c.min_tiles = s.paged ? 2 : 4;
     const int64_t units = std::max<int64_t>(1, (s.tokens + c.unit_tokens - 1) / c.unit_tokens) * s.Hkv;
     const int64_t keys = s.paged ? (int64_t)s.max_pages * s.page_size : s.key_tokens;
-    c.fold_floats = keys > kFoldHalves * kHalf ? (size_t)kMaxCtas * 2 * kRows * (s.d + 4) : 0;
+    c.carry_floats = keys > kPieceHalves * kHalf ? (size_t)kMaxCtas * 2 * kRows * (s.d + 8) : 0;
     c.max_parts = (int)std::min<int64_t>(kMaxParts, std::max<int64_t>(1, (4 * kSms + units - 1) / units));
     return c;
 }
@@ -991,7 +980,7 @@ FullCut full_tc_cut(const FullShape &s) {
 cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut &c,
                            const FullPlan *plan, const FullSeq *seqs, const void *Q,
                            const void *K, const void *V, void *O, float *lse, float *part_o,
-                           float *part_lse, float *fold, uint32_t *err, cudaStream_t st) {
+                           float *part_lse, float *carry, uint32_t *err, cudaStream_t st) {
     TcArgs a;
     a.s = s; a.q = q; a.c = c;
     a.plan = plan; a.seqs = seqs;
@@ -1004,11 +993,7 @@ cudaError_t launch_full_tc(const FullShape &s, const FullSeqs &q, const FullCut 
     a.wide = ((uintptr_t)O & 31u) == 0;
     a.scale_log2 = s.scale * kLog2e;
     a.lag = kMaxLag / a.scale_log2;
-    a.fold = fold;
-    // A stream without keys and the value check sit an item out: its key run
-    // can be the whole capacity.  A tile takes 1 to 3 us; 20 are allowed.
-    const int64_t keys = s.paged ? (int64_t)s.max_pages * s.page_size : s.key_tokens;
-    a.run_ns = tc::kWaitLimitNs + (uint64_t)(keys / kFullKeys) * 20000;
+    a.carry = carry;
     a.box = kFullKeys;                   // the largest power of two that divides pages and tiles
     if (s.paged)
         while (s.page_size % a.box != 0) a.box /= 2;

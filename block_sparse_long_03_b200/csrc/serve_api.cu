@@ -174,7 +174,7 @@ FullCut full_cut(const FullShape &s) {
 
 // Workspace: [error word][plan][sequences][partial O][partial lse][sums of long key runs]
 struct FullLayout {
-    size_t plan, seqs, part_o, part_lse, fold, total;
+    size_t plan, seqs, part_o, part_lse, carry, total;
 };
 FullLayout full_layout(const FullShape &s, const FullCut &c) {
     FullLayout L;
@@ -184,7 +184,7 @@ FullLayout full_layout(const FullShape &s, const FullCut &c) {
     const size_t rows = c.max_parts > 1 ? (size_t)c.max_parts * 2 * s.tokens * s.Hq : 0;
     L.part_o = o;   o += align_up(rows * s.d * sizeof(float));
     L.part_lse = o; o += align_up(rows * sizeof(float));
-    L.fold = o;     o += align_up(c.fold_floats * sizeof(float));
+    L.carry = o;     o += align_up(c.carry_floats * sizeof(float));
     L.total = o;
     return L;
 }
@@ -238,7 +238,7 @@ msa_status_t run_full(const msa_attn_params_t *params, bool paged, const void *Q
     float *part_o = (float *)(ws + L.part_o), *part_lse = (float *)(ws + L.part_lse);
     if (done == cudaSuccess)
         done = launch_full_tc(s, q, c, plan, seqs, Q, K, V, O, lse, part_o, part_lse,
-                              (float *)(ws + L.fold), err, st);
+                              (float *)(ws + L.carry), err, st);
     if (done == cudaSuccess && c.max_parts > 1)
         done = launch_full_combine(s, q, c, plan, seqs, part_o, part_lse, O, lse, st);
     return cuda_status(done);

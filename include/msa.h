@@ -598,9 +598,7 @@ MSA_EXPORT int64_t msa_query_pieces(const msa_params_t *params, int which, int32
  * gives up the kernel records MSA_ERR_DEVICE_TIMEOUT in the error word of
  * `workspace` (at least 256 bytes, 256-byte aligned), releases its tensor
  * memory and returns; read the status with msa_get_device_error.  Every wait
- * of the library's kernels ends this way instead of hanging (limit 2 s; in the
- * full attention, waits that may last a whole key run have 20 us more for each
- * 128 keys a sequence may have).
+ * of the library's kernels ends this way (limit 2 s) instead of hanging.
  */
 MSA_EXPORT msa_status_t msa_selftest_wait_timeout(void *workspace, size_t workspace_bytes,
                                                   uint32_t limit_us, void *stream);

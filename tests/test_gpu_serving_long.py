@@ -102,7 +102,7 @@ def test_a_key_run_of_seconds():
     """A single token over 2^29 keys (on 16 pages, again and again) beside 2400 prompt tokens, which
     leave it one key run and one stream: 4 million tiles one after another, about 5 s, longer than the
     2 s that a wait on another role's next step may take.  The stream without keys and the check
-    of the values wait that long for their turn, and nothing may give up.  All scores are 0 and
+    of the values wait for their turn meanwhile, and nothing may give up.  All scores are 0 and
     the values constant: the sums of weights are exact in fp32 (multiples of 64 up to 2^29), those of
     equal values too, so that O is the value."""
     msa, page, d, Hq = _msa(), 256, 64, 64
@@ -138,3 +138,46 @@ def test_fp32_sums_of_equal_values(d):
     off = (O.double() / value.double() - 1).abs()
     assert float(off.max()) <= (31 + 2 ** 13 + 2) * 2.0 ** -24, float(off.max())
     assert float((lse.double() - math.log(L)).abs().max()) <= 2.0 ** -22 * math.log(L)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_odd_values_along_a_long_run(d):
+    """Infinite values and NaN, keys of -infinity and rows without weights, where a run of keys is
+    taken in pieces of 65536: in the first piece, at the end of one and in the last, under tokens
+    that attend them and tokens that do not."""
+    msa, g = _msa(), torch.Generator().manual_seed(d + 5)
+    n = 65536 + 65536 + 1000                           # keys; the last 2400 have queries
+    Q = torch.randn((T, HEADS, d), generator=g).to(BF16).cuda()
+    K, V = (torch.randn((n, 1, d), generator=g).to(BF16).cuda() for _ in range(2))
+    Q[..., 0], K[..., 0] = 1.0, 0.0
+    cq, ck = ref.offsets([T]).cuda(), ref.offsets([n]).cuda()
+    first = n - T
+    want, want_lse, ws = msa.attn_packed(Q, K, V, cq, ck)
+    assert msa.msa_get_device_error(ws) == 0 and bool(torch.isfinite(want).all())
+    at = [77, 65535, 65536, 131071, 131072, first + 1, first + 700, n - 1]
+    for key in at:                                     # an infinite value, every weight positive
+        V2 = V.clone()
+        V2[key, 0, 3], V2[key, 0, 5] = math.inf, math.nan
+        O, lse, _ = msa.attn_packed(Q, K, V2, cq, ck)
+        sees = max(0, key - first)                     # the first token that attends the key
+        assert torch.equal(O[:sees], want[:sees]) and torch.equal(lse, want_lse)
+        assert bool((O[sees:, :, 3] == math.inf).all()) and bool(torch.isnan(O[sees:, :, 5]).all())
+        keep = [c for c in range(d) if c not in (3, 5)]
+        assert torch.equal(O[..., keep], want[..., keep])
+    for lo, hi in ((0, 65536), (65536, 131072), (0, 131072)):   # pieces of zero weights
+        K2, V2 = K.clone(), V.clone()
+        K2[lo:hi, 0, 0] = -math.inf
+        O1, lse1, _ = msa.attn_packed(Q, K2, V, cq, ck)
+        dead = T - 1000 if hi == 131072 and lo == 0 else 0   # tokens that attend no other key
+        assert bool((O1[:dead] == 0).all()) and bool((lse1[:dead] == -math.inf).all())
+        assert bool(torch.isfinite(O1).all()) and bool(torch.isfinite(lse1[dead:]).all())
+        V2[lo + 9, 0, 3] = math.inf
+        O2, lse2, _ = msa.attn_packed(Q, K2, V2, cq, ck)
+        assert torch.equal(lse2, lse1) and torch.equal(O2[:dead], O1[:dead])
+        assert bool(torch.isnan(O2[dead:, :, 3]).all())
+        keep = [c for c in range(d) if c != 3]
+        assert torch.equal(O2[..., keep], O1[..., keep])
+    K2 = K.clone()
+    K2[1234] = math.nan                                # a NaN score in the first piece
+    O, lse, _ = msa.attn_packed(Q, K2, V, cq, ck)
+    assert bool(torch.isnan(O).all()) and bool(torch.isnan(lse).all())
