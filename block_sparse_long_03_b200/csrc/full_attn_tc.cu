@@ -26,14 +26,20 @@
 // The running maximum m that a row's P is taken against moves only when a
 // half's maximum would make P larger than 2^8: P keeps the same relative
 // rounding in bf16, far from fp32's range, and O is rarely rescaled.  The fp32
-// row sum is of the unrounded P.
+// row sum is of the unrounded P.  P is rounded to bf16 because one product's
+// operands have one type and V is bf16 (in fp32, or as two bf16 terms, the
+// product would cost two to four times as much): its errors, up to 2^-8 a weight
+// and independent of one another, leave O 1.2 to 1.4 times as far from the
+// 64-bit value as an fp32 computation that rounds once.  The exponentials are
+// ex2.approx, good to 2^-22, far under that.
 //
 // Measured (one B200 at its 1000 W limit, 1.65 to 1.8 GHz): one 32768-token
 // prompt of 32 heads, d = 128, 8.0 to 8.4 ms, 1.05 to 1.10 PFLOP/s on the
 // causal flops, 64 to 67 % of a measured 8192^3 matrix product; tensor pipe 53 %
 // busy, special-function units 53 %.  The products alone (no softmax) take
 // 6.2 to 6.8 ms of that, the softmax alone 5.9 to 6.5.  A decode step of 64
-// sequences of 2K to 16K keys: 440 us, 5.9 TB/s, 90 % of a copy.
+// sequences of 2K to 16K keys: 440 us for this kernel by itself, 5.9 TB/s, 90 %
+// of a copy (with the plan and the merge 466, the call in a loop 500).
 // Tried and slower: S released as soon as the softmax has it in registers, P
 // in columns of its own (8.5 ms); four softmax warpgroups, two a stream taking
 // halves in turn (8.9 ms); a quarter to a half of the exponentials as
@@ -594,7 +600,7 @@ __device__ __forceinline__ float row_max(const uint32_t (&v)[kHalf]) {
 
 // P = 2^(scale_log2 S - mb) of a half, as bf16 over S; returns the fp32 row
 // sum.  (A quarter of the exponentials as polynomials on the multiply-add pipe
-// gains nothing here: the special-function unit is busy 65 % of the time.)
+// gains nothing here: the special-function unit is busy 53 % of the time.)
 __device__ __forceinline__ float weights(const uint32_t (&v)[kHalf], uint32_t tP, uint64_t scale2,
                                          uint64_t mb2) {
     uint64_t l0 = 0, l1 = 0;                             // (0, 0)
@@ -956,13 +962,17 @@ cudaError_t launch_tc_t(const FullShape &s, const TcArgs &a, const void *Q, cons
 
 // Two row tiles of 128 / R tokens a unit.  Keys are split into runs while a
 // call has too few units to keep every SM busy several times over: about
-// kItemsPerSm items an SM (3, 4, 6, 8: a decode step of 64 sequences 485, 471,
-// 466, 474 us, a mixed step 1112, 1115, 1144, 1160 us; with page ids looked up
-// ahead, at four, 463 and 1075).  A run has at least two
+// kItemsPerSm items an SM (3, 4, 6, 8, on two workloads: a decode step of 64
+// sequences 485, 471, 466, 474 us, a mixed step 1112, 1115, 1144, 1160 us; with
+// page ids looked up ahead, at four, 463 and 1075).  A run has at least two
 // tiles over a paged cache, where a single token may have 1000 keys and every
 // SM idle (27 us; at least four: 31 us), and four over packed prompts, whose
 // shortest then need no merge (28.7 against 32.8 us).  The partial results
-// take at most (items + units) * 256 rows * 2, about 300 MB.
+// take at most (items + units) * 256 rows * 2, about 300 MB.  The number of runs
+// follows from the tokens of the whole call, not from a sequence's own: beside a
+// large chunk a single token has one run and one stream, whatever its length
+// (4096 tokens of 64 heads over 8 take 307 us, with a token over 128K keys beside
+// them 1.90 ms; that token alone 177 us).
 FullCut full_tc_cut(const FullShape &s) {
     constexpr int kItemsPerSm = 4, kSms = kMaxCtas;
     FullCut c;

@@ -172,7 +172,7 @@ FullCut full_cut(const FullShape &s) {
     return s.dtype == MSA_BF16 ? full_tc_cut(s) : full_simt_cut(s);
 }
 
-// Workspace: [error word][plan][sequences][partial O][partial lse][sums of long key runs]
+// Workspace: [error word][plan][sequences][partial O][partial lse][sums of long runs' pieces]
 struct FullLayout {
     size_t plan, seqs, part_o, part_lse, carry, total;
 };

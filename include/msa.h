@@ -400,9 +400,9 @@ MSA_EXPORT msa_status_t msa_decode_paged(const msa_params_t *params, const int32
  * every key.  Tokens are PACKED here: the tokens of all sequences lie one
  * after another, and cu_seqlens [B + 1] (int32, ascending) says that
  * sequence b's are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  Rows before
- * cu_seqlens[0] and from cu_seqlens[B] on belong to no sequence: they are not
- * read and their outputs are left as they were.  A sequence may have no
- * tokens.  Strides are in elements, from one token to the next (so that Q, K
+ * cu_seqlens[0] and from cu_seqlens[B] on belong to no sequence: what they
+ * hold does not matter (they may be read, like every row of the arrays) and
+ * their outputs are left as they were.  A sequence may have no tokens.  Strides are in elements, from one token to the next (so that Q, K
  * and V may be slices of one projection's output); 0 means dense; a token's
  * heads are dense.  They must keep every token 16-byte aligned.  Offset,
  * length, position and page arrays are 4-byte aligned, every other pointer as
